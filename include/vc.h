@@ -16,6 +16,11 @@
  *   acceptance        argmax of the K + 1 verifier logit rows, first mismatch,
  *                     accepted length and correction token (vc_accept).
  *
+ * A second quantised draft cache, in 4-bit floating point with a scale per 16
+ * channels of a token, is written token by token (vc_fp4_cache_write), read
+ * back (vc_fp4_cache_read) and drafted from (vc_draft_attn_fp4); layers whose
+ * attention has a sliding window are verified with vc_verify_attn_window.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Pointers are DEVICE pointers unless a parameter says "host".  The caller
@@ -281,6 +286,91 @@ VC_API vc_status vc_compact_kept(const vc_attn_shape* shape, const void* k, cons
                                  const int32_t* idx, int n_keep, void* k_out, void* v_out, void* ws,
                                  size_t ws_bytes, void* stream);
 
+/* ---- 4-bit floating-point draft cache -------------------------------------------
+ * One layer of a draft cache whose numbers are 4-bit floats (e2m1: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives) with one 8-bit float scale (e4m3) per
+ * block of 16 consecutive channels of one token's key or value row:
+ *
+ *   s     = e4m3(min(max_block |x| / 6, 448)), x = the row * 2^-exp[h]
+ *   code  = e2m1(x / s)   (|x| / s > 6 is stored as 6; s == 0: code 0)
+ *   x_hat = e2m1 value * s * 2^exp[h]
+ *
+ * both roundings to nearest, ties to the even code, decided as an exact
+ * division decides; a negative x that rounds to zero keeps its sign.  exp is
+ * an optional power of two per KV head that moves the head's values into the
+ * scales' range (about 0.02 .. 2688 as a block's largest value).  Every token
+ * is quantised by itself -- no group of tokens has to fill up first, unlike
+ * vc_quant_cache -- so a drafted token's row can be appended as soon as it is
+ * computed.  The pages fix no format (they see a compressor only through its
+ * bits per element); this one is this library's choice.
+ *
+ * Storage: 16 tokens form one RECORD of 18 * D bytes (token t = 0..15 of the
+ * record, channel c, block j = c / 16, even channel in a byte's low half):
+ *   records  uint8 [B][Hkv][T_cap / 16][18 * D]
+ *   [0, 8D)     key codes, [16][D/2]: byte t * D/2 + c/2
+ *   [8D, 16D)   value codes.  With gr = c / (D/8), x = c % (D/8) / 2:
+ *               D = 128: byte (t/8)*512 + gr*64 + (t%8/2)*16 + (t%2)*8 + x
+ *               D = 64:  byte gr*64 + (t%8/2)*16 + (t/8)*8 + (t%2)*4 + x
+ *   [16D, 17D)  key scales.   D = 128: byte (t%8)*16 + (j/2)*4 + (t/8)*2 + j%2
+ *                             D = 64:  byte (t%8)*8 + j*2 + t/8
+ *   [17D, 18D)  value scales: byte j*16 + (t%8/2)*4 + (t/8)*2 + t%2
+ * (the order in which the lanes of the draft kernel's matrix tiles read them:
+ * every lane's codes and scales are contiguous).
+ *
+ *   T_cap   capacity in tokens, a multiple of 16, 16 <= T_cap < 2^31
+ *   T       tokens held by every request when lens is NULL, 0 <= T <= T_cap
+ *   lens    optional device int32 [B]: tokens held by each request
+ *   k_exp, v_exp  optional device int32 [Hkv], clamped to [-60, 60]; NULL: 0
+ * T and lens matter to vc_draft_attn_fp4 only; bytes of tokens at or past a
+ * request's length may hold anything.  A length outside [0, T_cap] is treated
+ * as 0 and raises VC_FLAG_BAD_LENGTH. */
+typedef struct vc_fp4_cache {
+  void* records;
+  int64_t T_cap;
+  int64_t T;
+  const int32_t* lens;
+  const int32_t* k_exp;
+  const int32_t* v_exp;
+} vc_fp4_cache;
+
+/* vc_fp4_cache_write quantises rows as they are written: row i of k, v ([B][Hkv][n][D],
+ * dtype VC_BF16 or VC_F16) becomes token pos[b] + i of request b, for
+ * i < counts[b].  pos: device int32 [B], or NULL: pos0 for every request;
+ * counts: device int32 [B] in [0, n], or NULL: n.  Other tokens keep every
+ * byte.  Nothing else has to be updated after a round: rejected drafts are
+ * overwritten by the next write at their positions.
+ * vc_fp4_cache_read is the way back: tokens pos[b] + i, i < counts[b], go to
+ * row i of k_out, v_out ([B][Hkv][n][D], dtype VC_BF16, VC_F16 or VC_F32;
+ * x_hat is exact in VC_BF16 and VC_F32 and rounded once to VC_F16); rows
+ * i >= counts[b] are left as they were.
+ * A request with pos < 0, a count outside [0, n] or pos + count > T_cap is
+ * skipped and raises VC_FLAG_BAD_LENGTH; a NaN (stored as 0) or a block whose
+ * largest |x| exceeds 6 * 448 (stored as the nearest value in range) raises
+ * VC_FLAG_RANGE.  n >= 0; n == 0 does nothing.  B * Hkv <= 65535.  ws: a
+ * workspace of vc_compress_workspace_size() bytes (a flag word). */
+VC_API vc_status vc_fp4_cache_write(const vc_attn_shape* shape, const vc_fp4_cache* cache, const void* k, const void* v,
+                                    int dtype, int64_t n, const int32_t* pos, int64_t pos0, const int32_t* counts,
+                                    void* ws, size_t ws_bytes, void* stream);
+VC_API vc_status vc_fp4_cache_read(const vc_attn_shape* shape, const vc_fp4_cache* cache, void* k_out, void* v_out,
+                                   int dtype, int64_t n, const int32_t* pos, int64_t pos0, const int32_t* counts,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* vc_draft_attn_fp4: out[b][hq][:] = softmax(q . K_hat^T * sm_scale) . V_hat over the
+ * tokens of KV head hq / g that the newest token of request b sees.  With L =
+ * T or lens[b] that token sits at position L - 1 (its own row is written
+ * before the call) and sees token t < L if window == 0, t > L - 1 - window
+ * or t < n_sink: a sliding window of `window` tokens that includes the newest
+ * one, and the first n_sink tokens, which stay visible.
+ *   q    bf16 [B][Hq][D]        (|q| < 65504)
+ *   out  fp32 [B][Hq][D];  lse  fp32 [B][Hq] natural-log softmax
+ *        denominators, or NULL.  L == 0: a zero row, lse -inf.
+ *   window >= 0, n_sink >= 0 (without effect when window == 0).
+ *   ws   workspace of vc_draft_attn_fp4_workspace_size() bytes. */
+VC_API size_t vc_draft_attn_fp4_workspace_size(const vc_attn_shape* shape, const vc_fp4_cache* cache);
+VC_API vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window,
+                                   int64_t n_sink, const void* q, float* out, float* lse, void* ws, size_t ws_bytes,
+                                   void* stream);
+
 /* ---- cache maintenance around a round -----------------------------------------
  * After acceptance, a round keeps the accepted prefix plus the verifier's
  * correction and discards the rest of the draft (devshah.ca page, "The Core
@@ -322,6 +412,28 @@ VC_API vc_status vc_cache_commit(const vc_attn_shape* shape, const vc_quant_cach
 VC_API size_t vc_verify_attn_workspace_size(const vc_attn_shape* shape, int64_t T, int nq);
 VC_API vc_status vc_verify_attn(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T,
                          int nq, float* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- block verification attention with a sliding window ---------------------
+ * vc_verify_attn for layers whose attention is limited to a window, with
+ * first tokens that stay visible, and for requests of different lengths.
+ * With L = lens[b] (device int32 [B]; NULL: T) the block's own keys are rows
+ * L - nq .. L - 1 of request b; row i sits at position p = L - nq + i and
+ * sees key t <= p if window == 0, t > p - window or t < n_sink.  A row that
+ * sees no key (p < 0) gives a zero row and lse -inf.  Only rows of the union
+ * of the block's windows and of the first n_sink are read into a result:
+ * keys and values that no row sees may hold anything (NaN included); those
+ * that a row of the block sees must be finite.  T is the row stride between
+ * KV heads (the rows allocated); a length outside [0, T] is treated as 0 and
+ * raises VC_FLAG_BAD_LENGTH.
+ *   q    bf16 [B][nq][Hq][D];  k, v  bf16 [B][Hkv][T][D]
+ *   out  fp32 [B][nq][Hq][D];  lse   fp32 [B][nq][Hq] or NULL
+ *   1 <= nq <= 32, 1 <= T < 2^31, window >= 0, n_sink >= 0, g = Hq / Hkv <= 8,
+ *   D = 64 or 128, B * Hkv <= 65535. */
+VC_API size_t vc_verify_attn_window_workspace_size(const vc_attn_shape* shape, int64_t T, int nq, int64_t window,
+                                                   int64_t n_sink);
+VC_API vc_status vc_verify_attn_window(const vc_attn_shape* shape, const void* q, const void* k, const void* v,
+                                       int64_t T, const int32_t* lens, int nq, int64_t window, int64_t n_sink,
+                                       float* out, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- greedy acceptance -----------------------------------------------------
  * target[b][i] = argmax_v logits[b][i][v] for i = 0..K (lowest index wins a

@@ -44,9 +44,21 @@
 //     partial, which splitk_combine_kernel merges in a programmatic-dependent
 //     launch.
 // All waits are bounded; TMEM is always released.
+//
+// Sliding window (WIN, vc_verify_attn_window).  The same block runs over a
+// shorter list of key tiles: those of the first n_sink keys, then those from
+// the first key of the first row's window to the request's last key (one
+// list from key 0 when the two meet).  A tile starts at any key -- the key
+// coordinate of a tiled load has no alignment rule -- so the window's first
+// tile starts exactly at its first key.  The request's length is read on the
+// device, and its tiles are cut into C equal chunks there.  Value rows of a
+// tile that no row sees (past the request's length, or past the first n_sink
+// keys) may hold anything: the softmax warps clear them in shared memory
+// before P.V, since 0 * NaN would reach every row.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstring>
 #include <type_traits>
 
@@ -113,9 +125,32 @@ struct VArgs {
   // loop's waits
   int skip_k;
   uint64_t wait_ns;
+  // sliding window only
+  const int32_t* lens;
+  int64_t window, n_sink;
 };
 
-template <int D, int RTC>
+// Key tiles of one request under a sliding window: [0, ns) cover the first
+// n_sink keys, the others run from key w0 to key len.
+struct WinTiles {
+  int64_t len, w0, n_sink;
+  int ns, n;
+  __device__ WinTiles(int64_t len_, int nq, int64_t window, int64_t n_sink_) : len(len_), n_sink(n_sink_) {
+    w0 = window > 0 ? len - nq + 1 - window : 0;
+    if (w0 < 0) w0 = 0;
+    if (n_sink >= w0) {  // one list from key 0
+      w0 = 0;
+      ns = 0;
+    } else {
+      ns = static_cast<int>((n_sink + kVBN - 1) / kVBN);
+    }
+    n = ns + static_cast<int>((len - w0 + kVBN - 1) / kVBN);
+  }
+  __device__ int64_t start(int i) const { return i < ns ? static_cast<int64_t>(i) * kVBN : w0 + static_cast<int64_t>(i - ns) * kVBN; }
+  __device__ int64_t end(int i) const { return i < ns ? n_sink : len; }
+};
+
+template <int D, int RTC, bool WIN>
 __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                                      const __grid_constant__ CUtensorMap tm_k,
                                                                      const __grid_constant__ CUtensorMap tm_v,
@@ -154,9 +189,20 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
   const int i0 = rt * a.nqt;
   const int nq_t = max(0, min(a.nqt, a.nq - i0));
   const int M = nq_t * a.g;  // valid rows of this thread's row tile
-  const int64_t k_begin = static_cast<int64_t>(chunk) * a.tiles_per_chunk * kVBN;
-  const int64_t k_end = min(a.T, k_begin + static_cast<int64_t>(a.tiles_per_chunk) * kVBN);
-  const int ntiles = static_cast<int>((k_end - k_begin + kVBN - 1) / kVBN);
+  int64_t len = a.T;  // keys of this request
+  if constexpr (WIN) {
+    if (a.lens) len = __ldg(a.lens + b);
+    if (len < 0 || len > a.T) {
+      if (tid == 0) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
+      len = 0;
+    }
+  }
+  const WinTiles wt(len, a.nq, WIN ? a.window : 0, WIN ? a.n_sink : 0);
+  const int first_tile = WIN ? chunk * ((wt.n + a.C - 1) / a.C) : 0;  // of the request's list (WIN)
+  const int64_t k_begin = WIN ? 0 : static_cast<int64_t>(chunk) * a.tiles_per_chunk * kVBN;
+  const int64_t k_end = WIN ? 0 : min(a.T, k_begin + static_cast<int64_t>(a.tiles_per_chunk) * kVBN);
+  const int ntiles = WIN ? max(0, min((wt.n + a.C - 1) / a.C, wt.n - first_tile))
+                         : static_cast<int>((k_end - k_begin + kVBN - 1) / kVBN);
   const bool softmax_thread = tid < K::SOFTMAX;
   bool fail = false;
 
@@ -166,7 +212,7 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
   auto issue_load = [&](int i, int v) {
     unsigned char* dst = st_s + (i % NS) * C::STAGE_B + v * C::KV_B;
     uint64_t* bar = v ? &bar_v[i % NS] : &bar_k[i % NS];
-    const int y = static_cast<int>(k_begin + static_cast<int64_t>(i) * kVBN);
+    const int y = static_cast<int>(WIN ? wt.start(first_tile + i) : k_begin + static_cast<int64_t>(i) * kVBN);
     if (v == 0 && i == a.skip_k) return;  // failure-path test: this tile never lands
     mbar_arrive_expect_tx(bar, C::KV_B);
 #pragma unroll
@@ -223,7 +269,7 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
 
   // row state
   const int i_row = i0 + (r < M ? r / a.g : 0);
-  const int64_t vis_end = a.T - a.nq + i_row + 1;  // keys [0, vis_end) visible to this row
+  const int64_t vis_end = len - a.nq + i_row + 1;  // keys [0, vis_end) visible to this row
   float m_run = -INFINITY, l_run = 0.f;
 
   // Bounded wait that also gives up as soon as another thread of the block
@@ -323,11 +369,15 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < 32; ++j) sr[0][j] = sr[1][j] = 0u;
       }
-      const int64_t t0 = k_begin + static_cast<int64_t>(i) * kVBN;
-      const int64_t lim = min(vis_end, k_end) - t0;  // keys [t0, t0 + lim) are live
+      const int64_t t0 = WIN ? wt.start(first_tile + i) : k_begin + static_cast<int64_t>(i) * kVBN;
+      const int64_t t_end = WIN ? wt.end(first_tile + i) : k_end;
+      const int64_t lim = min(vis_end, t_end) - t0;  // keys [t0, t0 + lim) are live
+      // sliding window: of those, keys below t0 + sink or from t0 + wlo on
+      const int64_t sink = WIN ? a.n_sink - t0 : 0;
+      const int64_t wlo = WIN && a.window > 0 ? vis_end - a.window - t0 : 0;
       // raw scores; the scale (> 0) is applied in the exponent's FMA below
       float tmax = -INFINITY;
-      if (__all_sync(FULL, lim >= kVBN)) {  // whole tile visible to the warp's rows: no mask
+      if (__all_sync(FULL, lim >= kVBN && (!WIN || sink >= kVBN || wlo <= 0))) {  // whole tile visible to the warp's rows: no mask
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -337,7 +387,9 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float x = (c * 32 + j < lim) ? __uint_as_float(sr[c][j]) : -INFINITY;
+            const int key = c * 32 + j;
+            const bool seen = key < lim && (!WIN || key < sink || key >= wlo);
+            const float x = seen ? __uint_as_float(sr[c][j]) : -INFINITY;
             sr[c][j] = __float_as_uint(x);
             tmax = fmaxf(tmax, x);
           }
@@ -371,6 +423,23 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
           plo[c * 16 + j / 2] = pack_bf2(lo.x, lo.y);
         }
       l_run = l_run * alpha + psum;
+      if constexpr (WIN) {
+        // value rows that no row sees: cleared once the tile has landed (rows
+        // past T are zeros already), before this warp's arrival on bar_p
+        if (t_end < a.T && t_end - t0 < kVBN) {
+          if (!fail && !wait_or_abort(&bar_v[i % NS], (i / NS) & 1)) fail = true;
+          if (!fail) {
+            unsigned char* vs = st_s + (i % NS) * C::STAGE_B + C::KV_B;
+            const int dead = static_cast<int>(t_end - t0);
+            for (int e = tid; e < (kVBN - dead) * (D / 8); e += K::SOFTMAX) {
+              const int row = dead + e / (D / 8), ch = e % (D / 8);
+              *reinterpret_cast<uint4*>(vs + (ch >> 3) * (kVBN * 128) + row * 128 + (ch & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+      }
       // O is rescaled only when a row of the warp raised its maximum (rare
       // with the lazy rule); only then must the previous P.V be done first.
       // P goes over this tile's own S buffer, which no MMA in flight reads,
@@ -646,7 +715,7 @@ struct VPlan {
 
 // Resident blocks per SM of one instance (cached per device; also sets the
 // kernel's shared-memory attribute on that device).
-template <int D, int RTC>
+template <int D, int RTC, bool WIN>
 int verify_occupancy() {
   using C = VCfg<D, RTC>;
   static int cache[64] = {0};
@@ -654,9 +723,9 @@ int verify_occupancy() {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (cache[dev] == 0) {
-    cudaFuncSetAttribute(verify_kernel<D, RTC>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_B);
+    cudaFuncSetAttribute(verify_kernel<D, RTC, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_B);
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, verify_kernel<D, RTC>, VBlk<RTC>::THREADS, C::SMEM_B) !=
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, verify_kernel<D, RTC, WIN>, VBlk<RTC>::THREADS, C::SMEM_B) !=
             cudaSuccess ||
         n < 1)
       n = 1;
@@ -669,7 +738,8 @@ int verify_occupancy() {
 // minimises waves x (tiles per chunk + 2), where a wave is SMs x resident
 // blocks and the 2 stands for a block's fixed cost (its query load, pipeline
 // fill and partial write).
-VPlan plan_verify(const vc_attn_shape& sh, int64_t T, int nq) {
+template <bool WIN>
+VPlan plan_tiles(const vc_attn_shape& sh, int64_t tiles, int nq) {
   VPlan p{};
   const int g = sh.Hq / sh.Hkv;
   p.nqt = 128 / g;
@@ -684,9 +754,8 @@ VPlan plan_verify(const vc_attn_shape& sh, int64_t T, int nq) {
   // tensor pipe's round trips, not by HBM, so it pays off only when the
   // separate blocks' second read of K/V is what limits them.
   p.RTC = (p.RT == 2 && units <= 16) ? 2 : 1;
-  const int64_t tiles = (T + kVBN - 1) / kVBN;
-  const int occ = p.RTC == 2 ? (sh.D == 128 ? verify_occupancy<128, 2>() : verify_occupancy<64, 2>())
-                             : (sh.D == 128 ? verify_occupancy<128, 1>() : verify_occupancy<64, 1>());
+  const int occ = p.RTC == 2 ? (sh.D == 128 ? verify_occupancy<128, 2, WIN>() : verify_occupancy<64, 2, WIN>())
+                             : (sh.D == 128 ? verify_occupancy<128, 1, WIN>() : verify_occupancy<64, 1, WIN>());
   const int64_t slots = static_cast<int64_t>(occ) * sm_count();
   const int64_t n = static_cast<int64_t>(units) * (p.RT / p.RTC);
   int64_t c = 1, best = -1;
@@ -707,6 +776,23 @@ VPlan plan_verify(const vc_attn_shape& sh, int64_t T, int nq) {
   p.off_o = align_up(p.off_ml + nunit * p.C * rows * 2 * 4, 256);
   p.total = align_up(p.off_o + nunit * p.C * rows * sh.D * 4, 256);
   return p;
+}
+
+VPlan plan_verify(const vc_attn_shape& sh, int64_t T, int nq) {
+  return plan_tiles<false>(sh, (T + kVBN - 1) / kVBN, nq);
+}
+
+// Most key tiles that a request of up to T keys has under the window: those of
+// the first keys and of the rows' windows, each rounded up.
+VPlan plan_verify_window(const vc_attn_shape& sh, int64_t T, int nq, int64_t window, int64_t n_sink) {
+  const int64_t all = (T + kVBN - 1) / kVBN;
+  int64_t tiles = all;
+  if (window > 0 && window < T) {
+    const int64_t sinks = ((n_sink < T ? n_sink : T) + kVBN - 1) / kVBN;
+    const int64_t own = sinks + (window + nq - 1 + kVBN - 1) / kVBN;
+    tiles = own < all + 1 ? own : all + 1;
+  }
+  return plan_tiles<true>(sh, tiles, nq);
 }
 
 vc_status check_verify(const vc_attn_shape* sh, int64_t T, int nq, const char* who) {
@@ -734,21 +820,26 @@ size_t vc_verify_attn_workspace_size(const vc_attn_shape* shape, int64_t T, int 
 
 namespace vc {
 namespace {
-vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T, int nq,
-                        float* out, float* lse, void* ws, size_t ws_bytes, void* stream, int skip_k,
-                        uint64_t wait_ns) {
-  vc_status st = vc::check_verify(shape, T, nq, "vc_verify_attn");
+// WIN: plan and launch of vc_verify_attn_window (arguments checked by the caller).
+template <bool WIN>
+vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T,
+                        const int32_t* lens, int nq, int64_t window, int64_t n_sink, float* out, float* lse, void* ws,
+                        size_t ws_bytes, void* stream, int skip_k, uint64_t wait_ns) {
+  const char* who = WIN ? "vc_verify_attn_window" : "vc_verify_attn";
+  vc_status st = vc::check_verify(shape, T, WIN ? 1 : nq, who);
   if (st != VC_OK) return st;
-  VC_REQUIRE(q && k && v && out && ws, "vc_verify_attn: null pointer argument");
+  VC_REQUIRE(nq >= 1 && nq <= 32, "%s: need 1 <= nq <= 32 (got %d)", who, nq);
+  VC_REQUIRE(q && k && v && out && ws, "%s: null pointer argument", who);
   VC_REQUIRE(vc::aligned16(q) && vc::aligned16(k) && vc::aligned16(v) && vc::aligned16(out) && vc::aligned16(ws),
-             "vc_verify_attn: q, k, v, out and workspace must be 16-byte aligned");
-  const vc::VPlan p = vc::plan_verify(*shape, T, nq);
-  VC_REQUIRE(ws_bytes >= p.total, "vc_verify_attn: workspace too small (%zu < %zu)", ws_bytes, p.total);
+             "%s: q, k, v, out and workspace must be 16-byte aligned", who);
+  const vc::VPlan p =
+      WIN ? vc::plan_verify_window(*shape, T, nq, window, n_sink) : vc::plan_verify(*shape, T, nq);
+  VC_REQUIRE(ws_bytes >= p.total, "%s: workspace too small (%zu < %zu)", who, ws_bytes, p.total);
   const int units = shape->B * shape->Hkv;
   CUtensorMap tq, tk, tv;
   if (!vc::make_kv_map(&tk, k, T, shape->D, units) || !vc::make_kv_map(&tv, v, T, shape->D, units) ||
       !vc::make_q_map(&tq, q, static_cast<int64_t>(shape->B) * nq, shape->Hq, shape->D, shape->Hq / shape->Hkv, p.nqt))
-    return vc::set_error(VC_ERR_CUDA, "vc_verify_attn: could not encode the Q/K/V tensor maps");
+    return vc::set_error(VC_ERR_CUDA, "%s: could not encode the Q/K/V tensor maps", who);
   char* w = static_cast<char*>(ws);
   vc::VArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -766,6 +857,9 @@ vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k
   a.flags = reinterpret_cast<uint32_t*>(w);
   a.skip_k = skip_k;
   a.wait_ns = wait_ns;
+  a.lens = lens;
+  a.window = window;
+  a.n_sink = n_sink;
   a.o.out = out;
   a.o.lse = lse;
   a.o.part_ml = reinterpret_cast<float*>(w + p.off_ml);
@@ -773,13 +867,13 @@ vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k
   CUtensorMap to;
   memset(&to, 0, sizeof(to));
   if (p.C > 1 && !vc::make_part_map(&to, a.o.part_o, p.nqt * a.g, shape->D, static_cast<int64_t>(units) * p.RT * p.C))
-    return vc::set_error(VC_ERR_CUDA, "vc_verify_attn: could not encode the partials' tensor map");
+    return vc::set_error(VC_ERR_CUDA, "%s: could not encode the partials' tensor map", who);
   dim3 grid(p.C, units, p.RT / p.RTC);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto go = [&](auto DD, auto RR) {
     constexpr int Dv = decltype(DD)::value, Rv = decltype(RR)::value;
-    vc::verify_occupancy<Dv, Rv>();  // sets the shared-memory attribute once per device
-    vc::verify_kernel<Dv, Rv><<<grid, vc::VBlk<Rv>::THREADS, vc::VCfg<Dv, Rv>::SMEM_B, s>>>(tq, tk, tv, to, a);
+    vc::verify_occupancy<Dv, Rv, WIN>();  // sets the shared-memory attribute once per device
+    vc::verify_kernel<Dv, Rv, WIN><<<grid, vc::VBlk<Rv>::THREADS, vc::VCfg<Dv, Rv>::SMEM_B, s>>>(tq, tk, tv, to, a);
   };
   using I128 = std::integral_constant<int, 128>;
   using I64 = std::integral_constant<int, 64>;
@@ -808,7 +902,7 @@ vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k
         vc::launch_splitk_combine<64>(a.o, p.C, rows_cap, n_rows, map, s);
     }
   }
-  return vc::launch_status("vc_verify_attn");
+  return vc::launch_status(who);
 }
 }  // namespace
 }  // namespace vc
@@ -817,7 +911,30 @@ extern "C" {
 
 vc_status vc_verify_attn(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T, int nq,
                          float* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
-  return vc::verify_launch(shape, q, k, v, T, nq, out, lse, ws, ws_bytes, stream, -1, 2000000000ull);
+  return vc::verify_launch<false>(shape, q, k, v, T, nullptr, nq, 0, 0, out, lse, ws, ws_bytes, stream, -1,
+                                  2000000000ull);
+}
+
+size_t vc_verify_attn_window_workspace_size(const vc_attn_shape* shape, int64_t T, int nq, int64_t window,
+                                            int64_t n_sink) {
+  const char* who = "vc_verify_attn_window_workspace_size";
+  if (vc::check_verify(shape, T, 1, who) != VC_OK) return 0;
+  if (nq < 1 || nq > 32 || window < 0 || n_sink < 0) {
+    vc::set_error(VC_ERR_INVALID_ARG, "%s: need 1 <= nq <= 32, window >= 0 and n_sink >= 0", who);
+    return 0;
+  }
+  return vc::plan_verify_window(*shape, T, nq, window, n_sink).total;
+}
+
+vc_status vc_verify_attn_window(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T,
+                                const int32_t* lens, int nq, int64_t window, int64_t n_sink, float* out, float* lse,
+                                void* ws, size_t ws_bytes, void* stream) {
+  VC_REQUIRE(window >= 0 && n_sink >= 0, "vc_verify_attn_window: window and n_sink must be >= 0");
+  // no position reaches 2^31: larger values mean the same and would overflow
+  window = std::min<int64_t>(window, int64_t(1) << 31);
+  n_sink = std::min<int64_t>(n_sink, int64_t(1) << 31);
+  return vc::verify_launch<true>(shape, q, k, v, T, lens, nq, window, n_sink, out, lse, ws, ws_bytes, stream, -1,
+                                 2000000000ull);
 }
 
 vc_status vc_debug_verify_abort(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T,
@@ -826,8 +943,8 @@ vc_status vc_debug_verify_abort(const vc_attn_shape* shape, const void* q, const
   VC_REQUIRE(skip_tile >= 0, "vc_debug_verify_abort: skip_tile must be >= 0 (got %d)", skip_tile);
   VC_REQUIRE(limit_ns >= 1000 && limit_ns <= 100000000,
              "vc_debug_verify_abort: limit must be 1 us .. 100 ms (got %lld ns)", static_cast<long long>(limit_ns));
-  return vc::verify_launch(shape, q, k, v, T, nq, out, lse, ws, ws_bytes, stream, skip_tile,
-                           static_cast<uint64_t>(limit_ns));
+  return vc::verify_launch<false>(shape, q, k, v, T, nullptr, nq, 0, 0, out, lse, ws, ws_bytes, stream, skip_tile,
+                                  static_cast<uint64_t>(limit_ns));
 }
 
 }  // extern "C"

@@ -51,6 +51,11 @@ class vc_sparse_cache(Structure):
     _fields_ = [("k", c_void_p), ("v", c_void_p), ("T_store", c_int64), ("idx", c_void_p), ("n_keep", c_int)]
 
 
+class vc_fp4_cache(Structure):
+    _fields_ = [("records", c_void_p), ("T_cap", c_int64), ("T", c_int64), ("lens", c_void_p), ("k_exp", c_void_p),
+                ("v_exp", c_void_p)]
+
+
 class vc_sched_request(Structure):
     _fields_ = [("shape", vc_attn_shape), ("draft_kind", c_int), ("qcaches", c_void_p), ("scaches", c_void_p),
                 ("draft_q", c_void_p), ("draft_out", c_void_p), ("draft_ws", c_void_p), ("draft_ws_bytes", c_size_t),
@@ -108,6 +113,17 @@ def lib() -> ctypes.CDLL:
             "vc_verify_attn_workspace_size": (c_size_t, [P(vc_attn_shape), c_int64, c_int]),
             "vc_verify_attn": (c_int, [P(vc_attn_shape), c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p,
                                        c_void_p, c_void_p, c_size_t, c_void_p]),
+            "vc_verify_attn_window_workspace_size": (c_size_t, [P(vc_attn_shape), c_int64, c_int, c_int64, c_int64]),
+            "vc_verify_attn_window": (c_int, [P(vc_attn_shape), c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                              c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_size_t,
+                                              c_void_p]),
+            "vc_fp4_cache_write": (c_int, [P(vc_attn_shape), P(vc_fp4_cache), c_void_p, c_void_p, c_int, c_int64,
+                                           c_void_p, c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
+            "vc_fp4_cache_read": (c_int, [P(vc_attn_shape), P(vc_fp4_cache), c_void_p, c_void_p, c_int, c_int64,
+                                          c_void_p, c_int64, c_void_p, c_void_p, c_size_t, c_void_p]),
+            "vc_draft_attn_fp4_workspace_size": (c_size_t, [P(vc_attn_shape), P(vc_fp4_cache)]),
+            "vc_draft_attn_fp4": (c_int, [P(vc_attn_shape), P(vc_fp4_cache), c_int64, c_int64, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_size_t, c_void_p]),
             "vc_accept_workspace_size": (c_size_t, [c_int, c_int, c_int]),
             "vc_accept": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                   c_void_p, c_size_t, c_void_p]),
@@ -176,6 +192,34 @@ def _p(x) -> int:
     return x.data_ptr()
 
 
+_I32 = (torch.int32,)
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_U8 = (torch.uint8,)
+_CODES = {torch.float32: VC_F32, torch.bfloat16: VC_BF16, torch.float16: VC_F16}
+
+
+def _arg(name: str, x, dtypes, n: int, optional: bool = False) -> int:
+    """Device pointer of a tensor argument after checking it: contiguous, on
+    the current device, of one of `dtypes` and of at least n elements.
+    Integers (raw device pointers) pass through."""
+    if x is None:
+        if optional:
+            return 0
+        raise ValueError(f"{name} is missing")
+    if isinstance(x, int):
+        return x
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {x.dtype})")
+    if x.numel() < n:
+        raise ValueError(f"{name} holds {x.numel()} elements, {n} are needed")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if x.get_device() < 0 or x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return x.data_ptr()
+
+
 def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
@@ -205,6 +249,28 @@ def sparse_cache(k, v, idx) -> vc_sparse_cache:
     """Descriptor of a token-dropped cache (keeps references to its tensors)."""
     d = vc_sparse_cache(_p(k), _p(v), int(k.shape[2]), _p(idx), int(idx.shape[-1]))
     d._keep = (k, v, idx)
+    return d
+
+
+def fp4_records(B: int, Hkv: int, T: int, D: int, device=None) -> torch.Tensor:
+    """Zero-filled records of a 4-bit floating-point cache for T tokens
+    (rounded up to whole records of 16): uint8 [B, Hkv, ceil(T / 16), 18 D]."""
+    return torch.zeros(B, Hkv, -(-int(T) // 16), 18 * D, dtype=torch.uint8, device=device or "cuda")
+
+
+def fp4_cache(records, T=None, lens=None, k_exp=None, v_exp=None) -> vc_fp4_cache:
+    """Descriptor of one layer of a 4-bit floating-point cache (layout in
+    include/vc.h): records uint8 [B, Hkv, T_cap / 16, 18 D]; T tokens held by
+    every request (default: the capacity) or lens, int32 [B], per request;
+    k_exp, v_exp optional int32 [Hkv].  Keeps references to its tensors."""
+    if records.dim() != 4 or records.shape[3] not in (18 * 64, 18 * 128):
+        raise ValueError("records must be [B, Hkv, T_cap / 16, 18 * D] with D = 64 or 128")
+    B, Hkv, n = records.shape[:3]
+    d = vc_fp4_cache(_arg("records", records, (torch.uint8,), records.numel()), n * 16, n * 16 if T is None else int(T),
+                     _arg("lens", lens, _I32, B, True), _arg("k_exp", k_exp, _I32, Hkv, True),
+                     _arg("v_exp", v_exp, _I32, Hkv, True))
+    d._keep = (records, lens, k_exp, v_exp)
+    d._dims = (B, Hkv, records.shape[3] // 18)
     return d
 
 
@@ -251,6 +317,67 @@ def vc_verify_attn_workspace_size(sh, T: int, nq: int) -> int:
 def vc_verify_attn(sh, q, k, v, T: int, nq: int, out, lse, ws, stream=None):
     _check(lib().vc_verify_attn(ctypes.byref(sh), _p(q), _p(k), _p(v), int(T), int(nq), _p(out), _p(lse), _p(ws),
                                 ws.numel() if hasattr(ws, "numel") else 1 << 62, _stream(stream)))
+
+
+def vc_verify_attn_window_workspace_size(sh, T: int, nq: int, window: int = 0, n_sink: int = 0) -> int:
+    return lib().vc_verify_attn_window_workspace_size(ctypes.byref(sh), int(T), int(nq), int(window), int(n_sink))
+
+
+def vc_verify_attn_window(sh, q, k, v, T: int, nq: int, out, lse, ws, window: int = 0, n_sink: int = 0, lens=None,
+                          stream=None):
+    """vc_verify_attn with a sliding window of `window` tokens (0: none), the
+    first n_sink tokens visible throughout and optional per-request lengths
+    (int32 [B]); see include/vc.h."""
+    nk, no = sh.B * sh.Hkv * int(T) * sh.D, sh.B * int(nq) * sh.Hq
+    _check(lib().vc_verify_attn_window(
+        ctypes.byref(sh), _arg("q", q, _BF16, no * sh.D), _arg("k", k, _BF16, nk), _arg("v", v, _BF16, nk), int(T),
+        _arg("lens", lens, _I32, sh.B, True), int(nq), int(window), int(n_sink), _arg("out", out, _F32, no * sh.D),
+        _arg("lse", lse, _F32, no, True), _arg("ws", ws, _U8, 0), ws.numel(), _stream(stream)))
+
+
+def _fp4_match(sh, fc):
+    if fc._dims != (sh.B, sh.Hkv, sh.D):
+        raise ValueError(f"the cache holds (B, Hkv, D) = {fc._dims}, the shape says {(sh.B, sh.Hkv, sh.D)}")
+
+
+def _fp4_rows(f, sh, fc, k, v, dtypes, n, ws, pos, pos0, counts, stream):
+    _fp4_match(sh, fc)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have the same dtype")
+    size = sh.B * sh.Hkv * int(n) * sh.D
+    _check(f(ctypes.byref(sh), ctypes.byref(fc), _arg("k", k, dtypes, size), _arg("v", v, dtypes, size),
+             _CODES[k.dtype], int(n), _arg("pos", pos, _I32, sh.B, True), int(pos0),
+             _arg("counts", counts, _I32, sh.B, True), _arg("ws", ws, _U8, 0), ws.numel(), _stream(stream)))
+
+
+def vc_fp4_cache_write(sh, fc, k, v, n: int, ws, pos=None, pos0: int = 0, counts=None, stream=None):
+    """Quantises rows k, v (bf16 or fp16 [B, Hkv, n, D]) into tokens
+    pos[b] + i, i < counts[b], of a 4-bit floating-point cache (pos, counts
+    int32 [B]; default pos0 and n for every request)."""
+    _fp4_rows(lib().vc_fp4_cache_write, sh, fc, k, v, (torch.bfloat16, torch.float16), n, ws, pos, pos0, counts,
+              stream)
+
+
+def vc_fp4_cache_read(sh, fc, n: int, k_out, v_out, ws, pos=None, pos0: int = 0, counts=None, stream=None):
+    """Tokens pos[b] + i, i < counts[b], of a 4-bit floating-point cache back
+    to rows i of k_out, v_out (bf16, fp16 or fp32 [B, Hkv, n, D])."""
+    _fp4_rows(lib().vc_fp4_cache_read, sh, fc, k_out, v_out, (torch.bfloat16, torch.float16, torch.float32), n, ws,
+              pos, pos0, counts, stream)
+
+
+def vc_draft_attn_fp4_workspace_size(sh, fc) -> int:
+    return lib().vc_draft_attn_fp4_workspace_size(ctypes.byref(sh), ctypes.byref(fc))
+
+
+def vc_draft_attn_fp4(sh, fc, q, out, ws, lse=None, window: int = 0, n_sink: int = 0, stream=None):
+    """Draft attention over a 4-bit floating-point cache, optionally limited
+    to a sliding window and the first n_sink tokens (see include/vc.h)."""
+    _fp4_match(sh, fc)
+    n = sh.B * sh.Hq
+    _check(lib().vc_draft_attn_fp4(ctypes.byref(sh), ctypes.byref(fc), int(window), int(n_sink),
+                                   _arg("q", q, _BF16, n * sh.D), _arg("out", out, _F32, n * sh.D),
+                                   _arg("lse", lse, _F32, n, True), _arg("ws", ws, _U8, 0), ws.numel(),
+                                   _stream(stream)))
 
 
 def vc_accept_workspace_size(B: int, K: int, V: int) -> int:

@@ -30,7 +30,7 @@
 // n_sink tokens, then those of the window).  The stages of all units form
 // one axis that the blocks cut into equal shares, whatever the requests'
 // lengths (read on the device): a share holds part of one unit, whole units,
-// and part of another.  The 4 warps of a block take a segment's stages
+// and part of another.  The 16 warps of a block take a segment's stages
 // round-robin, each through its own ring of bulk copies that runs ahead
 // across units.  A unit inside one share is written out at once; the others
 // leave one partial per block, merged by the block that finishes last.
@@ -42,23 +42,37 @@
 namespace vc {
 namespace {
 
-constexpr int kFWarps = 4;
+#ifndef FM
+#define FM 16
+#endif
+#ifndef FN
+#define FN 2
+#endif
+constexpr int kFWarps = 16;
 constexpr int kFThreads = kFWarps * 32;
-constexpr int kFBlocksPerSm = 4;
-constexpr int kFMinStages = 4;   // stages a block takes at least (one per warp)
+constexpr int kFMaxBlocks = 160;  // one per SM; partials of one unit that a merge takes
+constexpr int kFMinStages = FM;   // stages a block takes at least
 constexpr float kFBelow = 11.f;  // m is set this far below the largest score
+constexpr float kFNone = -3e38f; // m before any score (finite: -inf + -m stays -inf)
 constexpr float kFMost = 15.f;   // a score this far above m moves it: P <= 2^15
 
-template <int D>
+template <int D, bool HALF>
 struct FCfg {
   static constexpr int REC = fp4::Rec<D>::BYTES;
   static constexpr int NR = 256 / D;        // records per stage: 32 (D = 128) or 64 tokens
   static constexpr int STAGE = NR * REC;    // 4608 bytes
-  static constexpr int NST = 3;             // ring depth of a warp
+  static constexpr int NST = FN;            // ring depth of a warp
   static constexpr int RING = NST * STAGE;
   static constexpr int BAR_OFF = kFWarps * RING;
-  static constexpr int SMEM_B = BAR_OFF + kFWarps * NST * 8;
-  static_assert(8 * D * 4 <= STAGE, "a consumed stage holds a warp's state");
+  // a warp's state, fp32 [heads][OS] in the order of store_out's positions (the
+  // padding keeps its stores free of bank conflicts)
+  static constexpr int OS = D + 4;
+  static constexpr int STATE = (HALF ? 4 : 8) * OS * 4;
+  static constexpr int STATE_OFF = BAR_OFF + (kFWarps * NST * 8 + 15) / 16 * 16;
+  static constexpr int SMEM_B = STATE_OFF + kFWarps * STATE;
+  // the final merge's buffers take the ring's place
+  static constexpr int ML_B = kFMaxBlocks * 8 * 8;
+  static_assert(ML_B + kFThreads * 16 <= BAR_OFF, "merge buffers");
 };
 
 struct FArgs {
@@ -69,7 +83,8 @@ struct FArgs {
   const int32_t* lens;
   const int32_t* k_exp;
   const int32_t* v_exp;
-  int64_t T_cap, T, window, n_sink;
+  int64_t T_cap;
+  uint32_t T, window, n_sink;  // below 2^31
   int B, Hq, Hkv, g;
   float scale_log2;
   uint32_t* flags;
@@ -79,63 +94,67 @@ struct FArgs {
 };
 
 // One request's visible records as stages: [0, ns) cover records [0, rs),
-// the others records [r0, r1).  A request without tokens has one stage
-// without records, so that every unit is in some block's share.
+// the others records [r0, r1).  All tokens of stages [f0, f1) are visible.  A
+// request without tokens has one stage without records, so that every unit is
+// in some block's share.
 struct Span {
-  int64_t L, lo;  // length; first token of the window
-  int rs, r0, r1, ns, n;
+  uint32_t L, lo;  // length; first token of the window
+  int rs, r0, r1, ns, n, f0, f1;
 };
 
-__host__ __device__ inline Span make_span(int64_t L, int64_t window, int64_t n_sink, int NR) {
+__host__ __device__ inline Span make_span(uint32_t L, uint32_t window, uint32_t n_sink, int NR) {
   Span p;
   p.L = L;
   p.lo = window > 0 && L > window ? L - window : 0;
-  const int64_t sinks = n_sink < p.lo ? n_sink : p.lo;
+  const uint32_t sinks = n_sink < p.lo ? n_sink : p.lo;
   p.rs = static_cast<int>((sinks + fp4::kTok - 1) / fp4::kTok);
   p.r0 = static_cast<int>(p.lo / fp4::kTok);
   p.r1 = static_cast<int>((L + fp4::kTok - 1) / fp4::kTok);
   if (p.rs >= p.r0) p.rs = p.r0 = 0;  // the two meet: one list from record 0
   p.ns = (p.rs + NR - 1) / NR;
   p.n = p.ns + (p.r1 - p.r0 + NR - 1) / NR;
+  p.f0 = p.ns + static_cast<int>((p.lo - p.r0 * fp4::kTok + NR * fp4::kTok - 1) / (NR * fp4::kTok));
+  p.f1 = p.ns + (static_cast<int>(L / fp4::kTok) - p.r0) / NR;
   if (p.n == 0) p.n = 1;
   return p;
 }
 
 template <int D>
 __device__ __forceinline__ Span request_span(const FArgs& a, int b) {
-  int64_t L = a.T;
+  uint32_t L = a.T;
   if (a.lens) {
-    L = __ldg(a.lens + b);
-    if (L < 0 || L > a.T_cap) L = 0;
+    L = static_cast<uint32_t>(__ldg(a.lens + b));
+    if (L > a.T_cap) L = 0;  // (a negative length too)
   }
-  return make_span(L, a.window, a.n_sink, FCfg<D>::NR);
+  return make_span(L, a.window, a.n_sink, 256 / D);
 }
 
-// A warp's place on the stage axis: stage s of unit (b, h), whose first stage
-// is `start` stages after the block's first one; the block's part of the unit
-// ends at stage `end`.
 template <int D>
-struct Cursor {
-  Span p;
-  int b, h, start, s, end;
+__device__ __forceinline__ int stage_record(const Span& p, int s) {
+  return s < p.ns ? s * 256 / D : p.r0 + (s - p.ns) * 256 / D;
+}
+template <int D>
+__device__ __forceinline__ int stage_records(const Span& p, int s) {
+  return min(256 / D, (s < p.ns ? p.rs : p.r1) - stage_record<D>(p, s));
+}
 
-  __device__ __forceinline__ int begin() const { return start < 0 ? -start : 0; }
-  __device__ __forceinline__ void clip(int share) { end = min(p.n, share - start); }
-  __device__ __forceinline__ bool valid(int share) const { return start < share; }
-  __device__ __forceinline__ void next_unit(const FArgs& a, int share) {
-    start += p.n;
-    if (++h == a.Hkv) {
-      h = 0;
-      ++b;
-      if (start < share) p = request_span<D>(a, b);
-    }
-    clip(share);
-  }
-  __device__ __forceinline__ int record() const { return s < p.ns ? s * FCfg<D>::NR : p.r0 + (s - p.ns) * FCfg<D>::NR; }
-  __device__ __forceinline__ int records() const {
-    return min(FCfg<D>::NR, (s < p.ns ? p.rs : p.r1) - record());
+// The cut of W stages into nb shares: share k starts at stage first(k).
+struct Cut {
+  uint32_t q, r;
+  __device__ Cut(uint32_t W, uint32_t nb) : q(W / nb), r(W - W / nb * nb) {}
+  __device__ uint32_t first(uint32_t k) const { return k * q + min(k, r); }
+  __device__ uint32_t share_of(uint32_t x) const {  // that holds stage x
+    const uint32_t big = r * (q + 1);
+    return x < big ? x / (q + 1) : r + (x - big) / q;
   }
 };
+
+// mma_f16 into zeros
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 
 __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
   uint32_t y;
@@ -146,9 +165,97 @@ __device__ __forceinline__ uint32_t movm_t(uint32_t x) {
 // (a & m) | (b & ~m)
 __device__ __forceinline__ uint32_t blend(uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); }
 
+// A warp's accumulators hold channel row * (D / 8) + 2 x + c at position
+// x * 16 + row * 2 + c (m-tile x, the lane's row, c = 0, 1); states and
+// partials stay in that order.  Stores positions pos .. pos + 3 of head hd of
+// unit (b, h), sum v with total (M, L).
+template <int D>
+__device__ __forceinline__ void store_row(const FArgs& a, int b, int h, int hd, int pos, const float4& v,
+                                          const float (&tot)[2]) {
+  const int64_t r = static_cast<int64_t>(b) * a.Hq + h * a.g + hd;
+  float* dst = a.out + r * D + (pos % 16) / 2 * (D / 8) + pos / 16 * 2;
+  const float f = tot[1] > 0.f ? fp4::two_to(a.v_exp, h, 1) / tot[1] : 0.f;
+  *reinterpret_cast<float2*>(dst) = make_float2(v.x * f, v.y * f);
+  *reinterpret_cast<float2*>(dst + D / 8) = make_float2(v.z * f, v.w * f);
+  if (a.lse && pos == 0) a.lse[r] = lse_from(tot[0], tot[1]);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = warp_max_xor(x, d);
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+
+// Merges the partials of one unit (first stage u0, n stages) into its output
+// rows; block-wide, buf: shared memory of FCfg::ML_B + 16 bytes per thread.
+// Written for few instructions rather than few cycles: this code, like the
+// rest of the prologue and epilogue, runs once per block, out of an empty
+// instruction cache.
+template <int D, int ML_B>
+__device__ __forceinline__ void merge_unit(const FArgs& a, const Cut cut, int unit, uint32_t u0, int n,
+                                           unsigned char* buf, float (*tot)[2]) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.g;
+  const uint32_t kf = cut.share_of(u0);
+  const int np = static_cast<int>(cut.share_of(u0 + n - 1) - kf) + 1;
+  const int first = 2 * kf + (u0 > cut.first(kf) ? 1 : 0);  // then slot 2 k of block k
+  auto at = [&](int i) { return i == 0 ? first : 2 * (static_cast<int>(kf) + i); };
+  float2* ml = reinterpret_cast<float2*>(buf);  // [np][g] (m, l), then (weight, -)
+  float4* sum = reinterpret_cast<float4*>(buf + ML_B);
+  __syncthreads();
+#pragma unroll 1
+  for (int e = tid; e < np * g; e += kFThreads) {
+    const int i = e / g;
+    ml[e] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at(i) * g + (e - i * g));
+  }
+  __syncthreads();
+  if (warp < g) {
+    float M = -INFINITY, L = 0.f;
+#pragma unroll 1
+    for (int i = lane; i < np; i += 32) M = fmaxf(M, ml[i * g + warp].x);
+    M = warp_max(M);
+#pragma unroll 1
+    for (int i = lane; i < np; i += 32) {
+      const float2 x = ml[i * g + warp];
+      const float w = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+      L += w * x.y;
+      ml[i * g + warp].x = w;
+    }
+    L = warp_sum(L);
+    if (lane == 0) tot[warp][0] = M, tot[warp][1] = L;
+  }
+  __syncthreads();
+  // thread groups take partials in turn, 4 positions a thread
+  const int items = g * D / 4, groups = kFThreads / items;
+  const int grp = tid / items, it = tid - grp * items, hd = it * 4 / D;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = grp < groups ? grp : np; i < np; i += groups) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(at(i)) * g * D) + it);
+    const float w = ml[i * g + hd].x;
+    v.x += w * x.x, v.y += w * x.y, v.z += w * x.z, v.w += w * x.w;
+  }
+  sum[tid] = v;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll 1
+    for (int i = 1; i < min(groups, np); ++i) {
+      const float4 x = sum[i * items + it];
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+    const int b = unit / a.Hkv, h = unit - b * a.Hkv;
+    store_row<D>(a, b, h, hd, it * 4 % D, v, tot[hd]);
+  }
+}
+
 template <int D, bool HALF>
-__global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FArgs a) {
-  using C = FCfg<D>;
+__global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
+  using C = FCfg<D, HALF>;
   using R = fp4::Rec<D>;
   constexpr int NR = C::NR;
   constexpr int KT = D / 16;  // k-steps of a score tile, m-tiles of the values
@@ -156,9 +263,9 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
   __shared__ int s_pre[kFThreads + 1];   // stages before each group of requests
   __shared__ int s_wsum[kFWarps];
   __shared__ float s_ml[kFWarps][8][2];  // (m, l) of each warp
-  __shared__ int s_at[kFWarps];          // where each warp's o is (-1: no stage)
-  __shared__ float s_fin[8][2];          // (M, L) of the merge
-  __shared__ int s_last;
+  __shared__ float s_f[kFWarps][8];      // its weight in the block's sum
+  __shared__ float s_tot[8][2];          // (M, L) of the sum
+  __shared__ int s_last[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = lane >> 2, i4 = lane & 3;
   unsigned char* ring = smem + warp * C::RING;
@@ -171,15 +278,14 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
-  // ---- this block's share of the stage axis
-  int64_t W;
+  // ---- this block's share of the stage axis (below 2^31 stages: they all have bytes in memory)
+  uint32_t W;
   const int per = (a.B + kFThreads - 1) / kFThreads;  // requests per group
-  int n_same = 0;
+  uint32_t n_same = 0;
   if (a.lens) {
     int mine = 0;
     for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-      const int64_t L = __ldg(a.lens + b);
-      if ((L < 0 || L > a.T_cap) && blockIdx.x == 0) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
+      if (blockIdx.x == 0 && static_cast<uint32_t>(__ldg(a.lens + b)) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
       mine += request_span<D>(a, b).n * a.Hkv;
     }
     int x = mine;
@@ -197,85 +303,104 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
     W = s_pre[kFThreads];
   } else {
     n_same = request_span<D>(a, 0).n;
-    W = static_cast<int64_t>(n_same) * a.B * a.Hkv;
+    W = n_same * a.B * a.Hkv;
   }
-  int64_t nb = (W + kFMinStages - 1) / kFMinStages;
-  if (nb > gridDim.x) nb = gridDim.x;
-  const int64_t k = blockIdx.x;
+  const uint32_t nb = min((W + kFMinStages - 1) / kFMinStages, gridDim.x);
+  const uint32_t k = blockIdx.x;
   if (k >= nb) return;
-  const int64_t w0 = k * W / nb;
-  const int share = static_cast<int>((k + 1) * W / nb - w0);
-  Cursor<D> cc;
+  const Cut cut(W, nb);
+  const uint32_t w0 = cut.first(k);
+  const int share = static_cast<int>(cut.first(k + 1) - w0);
+  // the place on the axis: unit (b, h), whose first stage is `start` stages
+  // after the share's first one
+  int b, h, start;
+  Span p;
   {
-    int64_t first;  // stage that unit (cc.b, 0) starts at
+    uint32_t first;  // stage that unit (b, 0) starts at
     if (a.lens) {
       int lo = 0, hi = kFThreads;  // group with s_pre[lo] <= w0 < s_pre[lo + 1]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s_pre[mid] <= w0) lo = mid; else hi = mid;
       }
-      cc.b = lo * per;
+      b = lo * per;
       first = s_pre[lo];
-      cc.p = request_span<D>(a, cc.b);
-      while (first + static_cast<int64_t>(cc.p.n) * a.Hkv <= w0) {
-        first += static_cast<int64_t>(cc.p.n) * a.Hkv;
-        cc.p = request_span<D>(a, ++cc.b);
+      p = request_span<D>(a, b);
+      while (first + p.n * a.Hkv <= w0) {
+        first += p.n * a.Hkv;
+        p = request_span<D>(a, ++b);
       }
     } else {
-      cc.b = static_cast<int>(w0 / (static_cast<int64_t>(n_same) * a.Hkv));
-      first = static_cast<int64_t>(cc.b) * n_same * a.Hkv;
-      cc.p = request_span<D>(a, cc.b);
+      b = w0 / (n_same * a.Hkv);
+      first = b * n_same * a.Hkv;
+      p = request_span<D>(a, b);
     }
-    cc.h = static_cast<int>((w0 - first) / cc.p.n);
-    cc.start = static_cast<int>(first + static_cast<int64_t>(cc.h) * cc.p.n - w0);
-    cc.clip(share);
+    h = (w0 - first) / p.n;
+    start = static_cast<int>(first + h * p.n) - static_cast<int>(w0);
   }
 
-  // ---- the warp's copies: next stage with records of this warp into the next slot
-  Cursor<D> ic = cc;
-  ic.s = ic.begin() + warp;
+  // ---- the warp's copies run ahead of its work: stage is of unit (ib, ih),
+  //      at isrc if it is below ifast (stages of NR records, one after the
+  //      other)
   const int64_t unit_bytes = a.T_cap / fp4::kTok * R::BYTES;
-  int islot = 0;
+  int ib = b, ih = h, istart = start, is = max(0, -start) + warp, ifast = 0, islot = 0;
+  const uint8_t* isrc = nullptr;
+  const uint64_t policy = l2_evict_first();  // the records are read once per call
   auto issue_next = [&]() {
-    for (;;) {
-      if (!ic.valid(share)) return;
-      if (ic.s < ic.end) {
-        const int n = ic.records();
-        if (n > 0) {
-          if (lane == 0) {
-            const uint32_t bytes = static_cast<uint32_t>(n) * C::REC;
-            mbar_arrive_expect_tx(&bars[islot], bytes);
-            bulk_g2s_once(ring + islot * C::STAGE,
-                          a.records + (static_cast<int64_t>(ic.b) * a.Hkv + ic.h) * unit_bytes +
-                              static_cast<int64_t>(ic.record()) * C::REC,
-                          bytes, &bars[islot]);
+    uint32_t bytes = C::STAGE;
+    if (is >= ifast) {  // look for the next stage with records
+      for (;;) {
+        if (istart >= share) return;
+        const Span ip = request_span<D>(a, ib);
+        const int end = min(ip.n, share - istart);
+        if (is < end) {
+          const int n = stage_records<D>(ip, is);
+          if (n > 0) {
+            bytes = static_cast<uint32_t>(n) * C::REC;
+            isrc = a.records + (static_cast<int64_t>(ib) * a.Hkv + ih) * unit_bytes +
+                   static_cast<int64_t>(stage_record<D>(ip, is)) * C::REC;
+            ifast = is < ip.ns ? 0 : min(end, ip.ns + (ip.r1 - ip.r0) / NR);
+            break;
           }
-          islot = islot + 1 == C::NST ? 0 : islot + 1;
-          ic.s += kFWarps;
-          return;
+          is += kFWarps;
+        } else {
+          istart += ip.n;
+          is = warp;
+          ifast = 0;
+          if (++ih == a.Hkv) ih = 0, ++ib;
         }
-        ic.s += kFWarps;
-      } else {
-        ic.next_unit(a, share);
-        ic.s = warp;  // later units start inside the share
       }
     }
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars[islot], bytes);
+      bulk_g2s_hint(ring + islot * C::STAGE, isrc, bytes, &bars[islot], policy);
+    }
+    islot = islot + 1 == C::NST ? 0 : islot + 1;
+    is += kFWarps;
+    isrc += kFWarps * C::STAGE;
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < C::NST; ++i) issue_next();
 
+  // hi lanes keep a weight's first 11 bits, lo lanes the rest: v = p * lo_f + ((p & mask) ^ lo_s)
+  const float lo_f = i4 < 2 ? 0.f : 1.f;
+  const uint32_t lo_s = i4 < 2 ? 0u : 0x80000000u;
   int slot = 0;
-  uint32_t phase = 0;  // bit i: parity of slot i's next completion
+  uint32_t phase = 0;  // parity of the slot's next completion
+  // the share's first and last unit when other blocks hold parts of them
+  int open[2] = {-1, -1}, open_n[2] = {0, 0};
+  uint32_t open_u0[2] = {0, 0};  // their first stage
   bool fail = false;
-  for (; cc.valid(share); cc.next_unit(a, share)) {
-    const int s0 = cc.begin();
-    const int unit = cc.b * a.Hkv + cc.h;
+#pragma unroll 1
+  while (start < share) {
+    const int s0 = max(0, -start), end = min(p.n, share - start);
+    const int unit = b * a.Hkv + h;
     // ---- query fragments: lane's head = its tile column, channels 4 i4 .. of each k-step
     uint32_t qf[2 * KT];
     float sc0, sc1;
     {
       const int head = HALF ? (row & 3) : row;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(cc.b) * a.Hq + cc.h * a.g + head) * D + i4 * (D / 4));
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.Hq + h * a.g + head) * D + i4 * (D / 4));
       uint32_t w[D / 8];
       float big = 0.f;
 #pragma unroll
@@ -299,38 +424,31 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
         qf[x] = pack_h2(f.x * up, f.y * up);
       }
       // floor: -inf (a masked score) times the factor stays -inf
-      const float sc = fmaxf(a.scale_log2 * fp4::two_to(a.k_exp, cc.h, 1) * __int_as_float((127 + e) << 23), 1e-37f);
+      const float sc = fmaxf(a.scale_log2 * fp4::two_to(a.k_exp, h, 1) * __int_as_float((127 + e) << 23), 1e-37f);
       sc0 = __shfl_sync(0xffffffffu, sc, 8 * i4);
       sc1 = __shfl_sync(0xffffffffu, sc, 8 * i4 + 4);
     }
     float acc[KT][4];
 #pragma unroll
     for (int x = 0; x < KT; ++x) acc[x][0] = acc[x][1] = acc[x][2] = acc[x][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    int state = -1;
+    float m0 = kFNone, m1 = kFNone, l0 = 0.f, l1 = 0.f;
 
-    for (cc.s = s0 + warp; cc.s < cc.end; cc.s += kFWarps) {
-      const int nrec = cc.records();
-      if (nrec <= 0) continue;
-      if (!fail && !mbar_wait_bounded(&bars[slot], (phase >> slot) & 1, a.flags)) fail = true;
-      if (__any_sync(0xffffffffu, fail)) {
+    for (int x = s0 + warp; x < end && !fail; x += kFWarps) {
+      const bool full = x >= p.f0 && x < p.f1;
+      if (!full && stage_records<D>(p, x) <= 0) break;  // a request without tokens
+      if (!__all_sync(0xffffffffu, mbar_try_wait_hint(&bars[slot], phase, 20000u)) &&
+          __any_sync(0xffffffffu, !mbar_wait_bounded(&bars[slot], phase, a.flags))) {
         fail = true;
         break;
       }
-      phase ^= 1u << slot;
       const unsigned char* st = ring + slot * C::STAGE;
-      state = slot;
-      slot = slot + 1 == C::NST ? 0 : slot + 1;
-      const int64_t t0 = static_cast<int64_t>(cc.record()) * fp4::kTok;
-      const int64_t t1 = t0 + NR * fp4::kTok;
-      const bool full = t1 <= cc.p.L && nrec == NR && (t0 >= cc.p.lo || t1 <= a.n_sink);
+      if (++slot == C::NST) slot = 0, phase ^= 1;
 
       // ---- scores
       float c[NR][4];
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const unsigned char* rec = st + r * C::REC;
-        c[r][0] = c[r][1] = c[r][2] = c[r][3] = 0.f;
         uint32_t ka[D / 32], kb[D / 32], sa[D / 64], sb[D / 64];  // token row, row + 8: codes, scales (both halves)
         if constexpr (D == 128) {
           const uint4 x = *reinterpret_cast<const uint4*>(rec + lane * 16);
@@ -358,15 +476,22 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
 #pragma unroll
           for (int x = 0; x < 4; ++x) oa[x] = hmul2(oa[x], sa[w / 2]), ob[x] = hmul2(ob[x], sb[w / 2]);
           const uint32_t f0[4] = {oa[0], ob[0], oa[1], ob[1]}, f1[4] = {oa[2], ob[2], oa[3], ob[3]};
-          mma_f16(c[r], f0, qf[4 * w], qf[4 * w + 1]);
+          if (w == 0)
+            mma_f16_zero(c[r], f0, qf[0], qf[1]);
+          else
+            mma_f16(c[r], f0, qf[4 * w], qf[4 * w + 1]);
           mma_f16(c[r], f1, qf[4 * w + 2], qf[4 * w + 3]);
         }
       }
-      auto seen = [&](int64_t t) { return t < cc.p.L && (t >= cc.p.lo || t < a.n_sink); };
+      auto seen = [&](uint32_t t) { return t < p.L && (t >= p.lo || t < a.n_sink); };
+      uint32_t t0 = 0;
+      int nrec = NR;
       if (!full) {
+        t0 = static_cast<uint32_t>(stage_record<D>(p, x)) * fp4::kTok;
+        nrec = stage_records<D>(p, x);
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          const int64_t t = t0 + r * fp4::kTok + row;
+          const uint32_t t = t0 + r * fp4::kTok + row;
           if (r >= nrec || !seen(t)) c[r][0] = c[r][1] = -INFINITY;
           if (r >= nrec || !seen(t + 8)) c[r][2] = c[r][3] = -INFINITY;
         }
@@ -391,13 +516,12 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
         // (past 2^22 the subtraction would round: m = the maximum itself)
         const float n0 = fmaxf(m0, fabsf(x0) < 4194304.f ? x0 - kFBelow : x0);
         const float n1 = fmaxf(m1, fabsf(x1) < 4194304.f ? x1 - kFBelow : x1);
-        const float al0 = m0 == -INFINITY ? 0.f : ex2(m0 - n0), al1 = m1 == -INFINITY ? 0.f : ex2(m1 - n1);
+        const float al0 = ex2(m0 - n0), al1 = ex2(m1 - n1);
         m0 = n0, m1 = n1;
         l0 *= al0, l1 *= al1;
 #pragma unroll
         for (int x = 0; x < KT; ++x) acc[x][0] *= al0, acc[x][2] *= al0, acc[x][1] *= al1, acc[x][3] *= al1;
       }
-      const float off0 = m0 == -INFINITY ? 0.f : -m0, off1 = m1 == -INFINITY ? 0.f : -m1;
 
       // ---- values
 #pragma unroll
@@ -405,17 +529,15 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
         uint32_t bh[2], bl[2];  // P of tokens 2 i4 (+ 1) and 8 more, column = row of the lane
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float p0 = ex2(fmaf(c[r][2 * x], sc0, off0)), p1 = ex2(fmaf(c[r][2 * x + 1], sc1, off1));
+          const float p0 = ex2(fmaf(c[r][2 * x], sc0, -m0)), p1 = ex2(fmaf(c[r][2 * x + 1], sc1, -m1));
           l0 += p0;
           l1 += p1;
-          const uint32_t hi = pack_h2(p0, p1);
-          const float2 f = unpack_h2(hi);
-          const uint32_t lo = pack_h2(p0 - f.x, p1 - f.y);
+          const uint32_t h0 = __float_as_uint(p0) & 0xffffe000u, h1 = __float_as_uint(p1) & 0xffffe000u;
           if constexpr (HALF) {
-            bh[x] = movm_t(i4 < 2 ? hi : lo);
+            bh[x] = movm_t(pack_h2(fmaf(p0, lo_f, __uint_as_float(h0 ^ lo_s)), fmaf(p1, lo_f, __uint_as_float(h1 ^ lo_s))));
           } else {
-            bh[x] = movm_t(hi);
-            bl[x] = movm_t(lo);
+            bh[x] = movm_t(pack_h2(__uint_as_float(h0), __uint_as_float(h1)));
+            bl[x] = movm_t(pack_h2(p0 - __uint_as_float(h0), p1 - __uint_as_float(h1)));
           }
         }
         const unsigned char* rec = st + r * C::REC;
@@ -433,7 +555,7 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
           sw = *reinterpret_cast<const uint32_t*>(rec + R::VS + (lane >> 3) * 16 + i4 * 4);
         }
         if (!full) {  // a hidden token's scale may be a NaN: 0 instead
-          const int64_t t = t0 + r * fp4::kTok + 2 * i4;
+          const uint32_t t = t0 + r * fp4::kTok + 2 * i4;
           uint32_t keep = 0;
           if (r < nrec) {
             if (seen(t)) keep |= 0xffu;
@@ -464,126 +586,101 @@ __global__ void __launch_bounds__(kFThreads, kFBlocksPerSm) draft_fp4_kernel(FAr
         }
       }
       __syncwarp();
-      if (cc.s + kFWarps < cc.end) issue_next();  // the segment's last slot takes the warp's state first
+      issue_next();
     }
 
-    // ---- the warp's state into its last consumed slot: o [head][chan]
-    if (fail) {  // no result: flagged
-      state = -1;
-      m0 = m1 = -INFINITY;
-    }
+    // ---- the warp's state, then the block's result for this unit: output
+    //      rows, or a partial
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
-    if (state >= 0) {
-      float* o = reinterpret_cast<float*>(ring + state * C::STAGE);
+    if (fail || m0 == kFNone) m0 = -INFINITY;
+    if (fail || m1 == kFNone) m1 = -INFINITY;
+    float* o = reinterpret_cast<float*>(smem + C::STATE_OFF + warp * C::STATE) + 2 * i4 * C::OS + row * 2;
 #pragma unroll
-      for (int x = 0; x < KT; ++x) {
-        if constexpr (HALF) {  // high + low part
+    for (int x = 0; x < KT; ++x) {
+      if constexpr (HALF) {  // high + low part
 #pragma unroll
-          for (int y = 0; y < 4; ++y) acc[x][y] += __shfl_xor_sync(0xffffffffu, acc[x][y], 2);
-        }
-        const int ch = row * (D / 8) + 2 * x;
-        if (!HALF || i4 < 2) {
-          *reinterpret_cast<float2*>(o + 2 * i4 * D + ch) = make_float2(acc[x][0], acc[x][2]);
-          *reinterpret_cast<float2*>(o + (2 * i4 + 1) * D + ch) = make_float2(acc[x][1], acc[x][3]);
-        }
+        for (int y = 0; y < 4; ++y) acc[x][y] += __shfl_xor_sync(0xffffffffu, acc[x][y], 2);
+      }
+      if (!HALF || i4 < 2) {
+        *reinterpret_cast<float2*>(o + x * 16) = make_float2(acc[x][0], acc[x][2]);
+        *reinterpret_cast<float2*>(o + C::OS + x * 16) = make_float2(acc[x][1], acc[x][3]);
       }
     }
     if (row == 0 && (!HALF || i4 < 2)) {
       s_ml[warp][2 * i4][0] = m0, s_ml[warp][2 * i4][1] = l0;
       s_ml[warp][2 * i4 + 1][0] = m1, s_ml[warp][2 * i4 + 1][1] = l1;
     }
-    if (lane == 0) s_at[warp] = state < 0 ? -1 : warp * C::RING + state * C::STAGE;
     __syncthreads();
-
-    // ---- the block's result for this unit: final, or a partial
-    const bool whole = cc.start >= 0 && cc.end == cc.p.n;
-    const int64_t my_slot = 2 * k + (cc.start > 0 ? 1 : 0);
-    const float vup = fp4::two_to(a.v_exp, cc.h, 1);
-    const int64_t row0 = static_cast<int64_t>(cc.b) * a.Hq + cc.h * a.g;
-    for (int e = tid; e < a.g * (D / 4); e += kFThreads) {
-      const int hd = e / (D / 4), ch = (e - hd * (D / 4)) * 4;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kFWarps; ++w) M = fmaxf(M, s_ml[w][hd][0]);
-      float L = 0.f;
+    if (warp < a.g) {
+      const float m = lane < kFWarps ? s_ml[lane][warp][0] : -INFINITY;
+      const float M = warp_max(m);
+      const float f = m == -INFINITY ? 0.f : ex2(m - M);
+      const float L = warp_sum(lane < kFWarps ? f * s_ml[lane][warp][1] : 0.f);
+      if (lane < kFWarps) s_f[lane][warp] = f;
+      if (lane == 0) s_tot[warp][0] = M, s_tot[warp][1] = L;
+    }
+    __syncthreads();
+    const bool whole = start >= 0 && end == p.n;
+    if (tid < a.g * (D / 4)) {
+      const int hd = tid / (D / 4), pos = (tid - hd * (D / 4)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+#pragma unroll 4
       for (int w = 0; w < kFWarps; ++w) {
-        const float mw = s_ml[w][hd][0];
-        if (mw == -INFINITY) continue;
-        const float f = ex2(mw - M);
-        L += f * s_ml[w][hd][1];
-        const float4 x = *reinterpret_cast<const float4*>(smem + s_at[w] + (hd * D + ch) * 4);
+        const float f = s_f[w][hd];
+        const float4 x = *reinterpret_cast<const float4*>(smem + C::STATE_OFF + w * C::STATE + (hd * C::OS + pos) * 4);
         v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
       }
       if (whole) {
-        const float n = L > 0.f ? vup / L : 0.f;
-        *reinterpret_cast<float4*>(a.out + (row0 + hd) * D + ch) = make_float4(v.x * n, v.y * n, v.z * n, v.w * n);
-        if (a.lse && ch == 0) a.lse[row0 + hd] = lse_from(M, L);
+        store_row<D>(a, b, h, hd, pos, v, s_tot[hd]);
       } else {
-        *reinterpret_cast<float4*>(a.part_o + (my_slot * a.g + hd) * D + ch) = v;
-        if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + (my_slot * a.g + hd) * 2) = make_float2(M, L);
+        const int64_t at = (2 * static_cast<int64_t>(k) + (start > 0 ? 1 : 0)) * a.g + hd;
+        *reinterpret_cast<float4*>(a.part_o + at * D + pos) = v;
+        if (pos == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(s_tot[hd][0], s_tot[hd][1]);
       }
     }
-    if (!whole) __threadfence();
     __syncthreads();
-    if (state >= 0) {  // the state's slot is free again
-      if (lane == 0) fence_proxy_async_smem();
-      __syncwarp();
-      if (!fail) issue_next();
+    if (!whole) {
+      if (start > 0)
+        open[1] = unit, open_u0[1] = w0 + start, open_n[1] = p.n;
+      else
+        open[0] = unit, open_u0[0] = w0 + start, open_n[0] = p.n;
     }
-    if (whole) continue;
-
-    // ---- the block that finishes a unit's last partial merges them
-    const int64_t p0 = w0 + cc.start, p1 = p0 + cc.p.n;  // the unit's stages
-    const int64_t kf = ((p0 + 1) * nb - 1) / W, kl = (p1 * nb - 1) / W;  // blocks that hold the first and the last one
-    if (tid == 0) s_last = atomicAdd(a.tickets + unit, 1u) == static_cast<uint32_t>(kl - kf);
-    __syncthreads();
-    if (!s_last) continue;
-    __threadfence();
-    const int64_t first = 2 * kf + (p0 > kf * W / nb ? 1 : 0);  // then 2 k of the others
-    const int np = static_cast<int>(kl - kf + 1);
-    auto at = [&](int p) { return p == 0 ? first : 2 * (kf + p); };
-    for (int hd = warp; hd < a.g; hd += kFWarps) {
-      float M = -INFINITY, L = 0.f;
-      for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(a.part_ml + (at(p) * a.g + hd) * 2));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) M = warp_max_xor(M, d);
-      for (int p = lane; p < np; p += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (at(p) * a.g + hd) * 2));
-        if (ml.x != -INFINITY) L += ex2(ml.x - M) * ml.y;
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-      if (lane == 0) s_fin[hd][0] = M, s_fin[hd][1] = L;
+    start += p.n;
+    if (++h == a.Hkv) {
+      h = 0;
+      if (start < share) p = request_span<D>(a, ++b);
     }
-    if (tid == 0) a.tickets[unit] = 0;
-    __syncthreads();
-    for (int e = tid; e < a.g * (D / 4); e += kFThreads) {
-      const int hd = e / (D / 4), ch = (e - hd * (D / 4)) * 4;
-      const float M = s_fin[hd][0], L = s_fin[hd][1];
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int p = 0; p < np; ++p) {
-        const int64_t sl = at(p) * a.g + hd;
-        const float mp = __ldcg(a.part_ml + sl * 2);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + sl * D + ch));
-        const float f = mp == -INFINITY ? 0.f : ex2(mp - M);
-        v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
-      }
-      const float n = L > 0.f ? vup / L : 0.f;
-      *reinterpret_cast<float4*>(a.out + (row0 + hd) * D + ch) = make_float4(v.x * n, v.y * n, v.z * n, v.w * n);
-      if (a.lse && ch == 0) a.lse[row0 + hd] = lse_from(M, L);
-    }
-    __syncthreads();  // s_fin and s_last are the next unit's
   }
   // after a wait that gave up, copies may still be in flight
   if (fail)
-    for (int i = 0; i < C::NST; ++i) mbar_wait_bounded(&bars[i], (phase >> i) & 1, nullptr, 100000000ull);
+    for (int i = 0; i < C::NST; ++i) mbar_wait_bounded(&bars[i], i < slot ? phase ^ 1 : phase, nullptr, 100000000ull);
+
+  // ---- the block that finishes a unit's last partial merges them
+  if (open[0] < 0 && open[1] < 0) return;
+  if (tid == 0) {  // the barrier above ordered the other threads' stores before this fence
+    __threadfence();
+    uint32_t t[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (open[i] >= 0) t[i] = atomicAdd(a.tickets + open[i], 1u);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s_last[i] = open[i] >= 0 && t[i] == cut.share_of(open_u0[i] + open_n[i] - 1) - cut.share_of(open_u0[i]);
+      if (s_last[i]) {
+        a.tickets[open[i]] = 0;
+        __threadfence();
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i)
+    if (s_last[i]) merge_unit<D, C::ML_B>(a, cut, i ? open[1] : open[0], i ? open_u0[1] : open_u0[0], i ? open_n[1] : open_n[0],
+                                 smem, s_tot);
 }
 
 vc_status check_draft(const vc_attn_shape* sh, const vc_fp4_cache* c, const char* who) {
@@ -606,7 +703,7 @@ struct FPlan {
 FPlan plan_draft(const vc_attn_shape& sh) {
   FPlan p;
   const int g = sh.Hq / sh.Hkv;
-  p.max_blocks = sm_count() * kFBlocksPerSm;
+  p.max_blocks = std::min(sm_count(), kFMaxBlocks);
   const size_t slots = 2 * static_cast<size_t>(p.max_blocks) * g;
   p.off_ml = align_up(sizeof(WsHeader) + static_cast<size_t>(sh.B) * sh.Hkv * 4, 256);
   p.off_o = align_up(p.off_ml + slots * 2 * 4, 256);
@@ -620,13 +717,13 @@ void launch_draft(const FArgs& a, int blocks, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    cudaFuncSetAttribute(draft_fp4_kernel<D, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, FCfg<D>::SMEM_B);
+    cudaFuncSetAttribute(draft_fp4_kernel<D, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, FCfg<D, HALF>::SMEM_B);
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kFThreads);
-  cfg.dynamicSmemBytes = FCfg<D>::SMEM_B;
+  cfg.dynamicSmemBytes = FCfg<D, HALF>::SMEM_B;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -666,10 +763,10 @@ vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cach
   a.k_exp = cache->k_exp;
   a.v_exp = cache->v_exp;
   a.T_cap = cache->T_cap;
-  a.T = cache->T;
-  // no position reaches 2^31: larger values mean the same and would overflow
-  a.window = std::min<int64_t>(window, int64_t(1) << 31);
-  a.n_sink = std::min<int64_t>(n_sink, int64_t(1) << 31);
+  a.T = static_cast<uint32_t>(cache->lens ? 0 : cache->T);
+  // no position reaches 2^31 - 1: larger values mean the same
+  a.window = static_cast<uint32_t>(std::min<int64_t>(window, INT32_MAX));
+  a.n_sink = static_cast<uint32_t>(std::min<int64_t>(n_sink, INT32_MAX));
   a.B = shape->B;
   a.Hq = shape->Hq;
   a.Hkv = shape->Hkv;
@@ -682,7 +779,7 @@ vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cach
   a.part_o = reinterpret_cast<float*>(w + p.off_o);
   // blocks for the most stages that the requests can have; the kernel leaves
   // out those that their real lengths do not fill
-  const vc::Span sp = vc::make_span(cache->lens ? cache->T_cap : cache->T, a.window, a.n_sink, 256 / shape->D);
+  const vc::Span sp = vc::make_span(static_cast<uint32_t>(cache->lens ? cache->T_cap : cache->T), a.window, a.n_sink, 256 / shape->D);
   const int64_t stages = (static_cast<int64_t>(sp.n) + 1) * shape->B * shape->Hkv;
   const int blocks = static_cast<int>(
       std::min<int64_t>(p.max_blocks, (stages + vc::kFMinStages - 1) / vc::kFMinStages));

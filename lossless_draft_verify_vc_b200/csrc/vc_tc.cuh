@@ -119,11 +119,7 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
 // An L2 cache policy that evicts the lines it tags first: for data read
 // once (a stream of K/V tiles), so that it does not push out what is read
 // again soon (the chunk partials that the merge reads back).
-__device__ __forceinline__ uint64_t l2_evict_first() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(p));
-  return p;
-}
+using vc::l2_evict_first;
 
 // tma_load_3d with an L2 cache policy (from l2_evict_first and the like).
 __device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar,

@@ -42,16 +42,15 @@
 namespace vc {
 namespace {
 
-#ifndef FM
-#define FM 16
-#endif
-#ifndef FN
-#define FN 2
-#endif
 constexpr int kFWarps = 16;
 constexpr int kFThreads = kFWarps * 32;
 constexpr int kFMaxBlocks = 160;  // one per SM; partials of one unit that a merge takes
-constexpr int kFMinStages = FM;   // stages a block takes at least
+// Measured on B200 (us of device time per call at 8 requests x 32K, 1 x 262K,
+// 4 x window 4096): a unit's begin -- query load, state, partial -- costs a
+// block about as much as 24 stages; counted as nothing the blocks that hold
+// parts of two units finish last: 66.0, 66.4, 22.5 against 61.5, 60.4, 15.7.
+constexpr int kFPad = 24;
+constexpr int kFMinStages = 40;  // padding and stages a block takes at least: a short unit (16 stages) stays whole
 constexpr float kFBelow = 11.f;  // m is set this far below the largest score
 constexpr float kFNone = -3e38f; // m before any score (finite: -inf + -m stays -inf)
 constexpr float kFMost = 15.f;   // a score this far above m moves it: P <= 2^15
@@ -61,7 +60,7 @@ struct FCfg {
   static constexpr int REC = fp4::Rec<D>::BYTES;
   static constexpr int NR = 256 / D;        // records per stage: 32 (D = 128) or 64 tokens
   static constexpr int STAGE = NR * REC;    // 4608 bytes
-  static constexpr int NST = FN;            // ring depth of a warp
+  static constexpr int NST = 2;             // ring depth of a warp
   static constexpr int RING = NST * STAGE;
   static constexpr int BAR_OFF = kFWarps * RING;
   // a warp's state, fp32 [heads][OS] in the order of store_out's positions (the
@@ -70,9 +69,8 @@ struct FCfg {
   static constexpr int STATE = (HALF ? 4 : 8) * OS * 4;
   static constexpr int STATE_OFF = BAR_OFF + (kFWarps * NST * 8 + 15) / 16 * 16;
   static constexpr int SMEM_B = STATE_OFF + kFWarps * STATE;
-  // the final merge's buffers take the ring's place
-  static constexpr int ML_B = kFMaxBlocks * 8 * 8;
-  static_assert(ML_B + kFThreads * 16 <= BAR_OFF, "merge buffers");
+  // the final merges' buffers take the ring's place
+  static_assert(2 * (kFMaxBlocks * 8 * 8 + kFThreads / 2 * 16) <= BAR_OFF, "merge buffers");
 };
 
 struct FArgs {
@@ -192,56 +190,73 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // Merges the partials of one unit (first stage u0, n stages) into its output
-// rows; block-wide, buf: shared memory of FCfg::ML_B + 16 bytes per thread.
-// Written for few instructions rather than few cycles: this code, like the
-// rest of the prologue and epilogue, runs once per block, out of an empty
-// instruction cache.
-template <int D, int ML_B>
-__device__ __forceinline__ void merge_unit(const FArgs& a, const Cut cut, int unit, uint32_t u0, int n,
+// rows, by one half of the block (t: thread of the half; buf, tot: shared
+// memory of the half).  Written for few instructions rather than few cycles:
+// this code, like the rest of the prologue and epilogue, runs once per block,
+// out of an empty instruction cache.
+constexpr int kFHalf = kFThreads / 2;
+constexpr int kFMergeB = kFMaxBlocks * 8 * 8 + kFHalf * 16;
+
+template <int D>
+__device__ __forceinline__ void merge_unit(const FArgs& a, const Cut cut, int unit, uint32_t u0, int n, int half, int t,
                                            unsigned char* buf, float (*tot)[2]) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = t >> 5, lane = t & 31;
   const int g = a.g;
   const uint32_t kf = cut.share_of(u0);
   const int np = static_cast<int>(cut.share_of(u0 + n - 1) - kf) + 1;
-  const int first = 2 * kf + (u0 > cut.first(kf) ? 1 : 0);  // then slot 2 k of block k
-  auto at = [&](int i) { return i == 0 ? first : 2 * (static_cast<int>(kf) + i); };
+  // slot of partial 0 (the unit is the first or the last one of its block), then 2 k of block k
+  const int first = 2 * kf + (u0 - kFPad > cut.first(kf) ? 1 : 0);
   float2* ml = reinterpret_cast<float2*>(buf);  // [np][g] (m, l), then (weight, -)
-  float4* sum = reinterpret_cast<float4*>(buf + ML_B);
-  __syncthreads();
-#pragma unroll 1
-  for (int e = tid; e < np * g; e += kFThreads) {
-    const int i = e / g;
-    ml[e] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at(i) * g + (e - i * g));
-  }
-  __syncthreads();
-  if (warp < g) {
-    float M = -INFINITY, L = 0.f;
-#pragma unroll 1
-    for (int i = lane; i < np; i += 32) M = fmaxf(M, ml[i * g + warp].x);
-    M = warp_max(M);
-#pragma unroll 1
-    for (int i = lane; i < np; i += 32) {
-      const float2 x = ml[i * g + warp];
-      const float w = x.x == -INFINITY ? 0.f : ex2(x.x - M);
-      L += w * x.y;
-      ml[i * g + warp].x = w;
-    }
-    L = warp_sum(L);
-    if (lane == 0) tot[warp][0] = M, tot[warp][1] = L;
-  }
-  __syncthreads();
-  // thread groups take partials in turn, 4 positions a thread
-  const int items = g * D / 4, groups = kFThreads / items;
-  const int grp = tid / items, it = tid - grp * items, hd = it * 4 / D;
+  float4* sum = reinterpret_cast<float4*>(buf + kFMaxBlocks * 8 * 8);
+  auto at = [&](int i) { return i == 0 ? first : 2 * (static_cast<int>(kf) + i); };
+  auto sync = [&]() { asm volatile("bar.sync %0, %1;\n" ::"r"(1 + half), "n"(kFHalf) : "memory"); };
+  // thread groups take partials in turn, 4 positions a thread, 8 loads in flight
+  const int items = g * D / 4, groups = kFHalf / items;
+  const int grp = t / items, it = t - grp * items, hd = it * 4 / D;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = grp < groups ? grp : np; i < np; i += groups) {
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(at(i)) * g * D) + it);
-    const float w = ml[i * g + hd].x;
-    v.x += w * x.x, v.y += w * x.y, v.z += w * x.z, v.w += w * x.w;
+#pragma unroll 1
+  for (int base = 0; base < np; base += 8 * groups) {
+    float4 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = base + j * groups + grp;
+      x[j] = grp < groups && i < np
+                 ? __ldcg(reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(at(i)) * g * D) + it)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (base == 0) {  // meanwhile the weights
+#pragma unroll 1
+      for (int e = t; e < np * g; e += kFHalf) {
+        const int i = e / g;
+        ml[e] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at(i) * g + (e - i * g));
+      }
+      sync();
+      if (warp < g) {
+        float M = -INFINITY, L = 0.f;
+#pragma unroll 1
+        for (int i = lane; i < np; i += 32) M = fmaxf(M, ml[i * g + warp].x);
+        M = warp_max(M);
+#pragma unroll 1
+        for (int i = lane; i < np; i += 32) {
+          const float2 y = ml[i * g + warp];
+          const float w = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+          L += w * y.y;
+          ml[i * g + warp].x = w;
+        }
+        L = warp_sum(L);
+        if (lane == 0) tot[warp][0] = M, tot[warp][1] = L;
+      }
+      sync();
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = base + j * groups + grp;
+      const float w = i < np && grp < groups ? ml[i * g + hd].x : 0.f;
+      v.x += w * x[j].x, v.y += w * x[j].y, v.z += w * x[j].z, v.w += w * x[j].w;
+    }
   }
-  sum[tid] = v;
-  __syncthreads();
+  sum[t] = v;
+  sync();
   if (grp == 0) {
 #pragma unroll 1
     for (int i = 1; i < min(groups, np); ++i) {
@@ -264,7 +279,7 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
   __shared__ int s_wsum[kFWarps];
   __shared__ float s_ml[kFWarps][8][2];  // (m, l) of each warp
   __shared__ float s_f[kFWarps][8];      // its weight in the block's sum
-  __shared__ float s_tot[8][2];          // (M, L) of the sum
+  __shared__ float s_tot[2][8][2];       // (M, L) of the sum
   __shared__ int s_last[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = lane >> 2, i4 = lane & 3;
@@ -286,7 +301,7 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
     int mine = 0;
     for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
       if (blockIdx.x == 0 && static_cast<uint32_t>(__ldg(a.lens + b)) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
-      mine += request_span<D>(a, b).n * a.Hkv;
+      mine += (request_span<D>(a, b).n + kFPad) * a.Hkv;
     }
     int x = mine;
 #pragma unroll
@@ -302,7 +317,7 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
     __syncthreads();
     W = s_pre[kFThreads];
   } else {
-    n_same = request_span<D>(a, 0).n;
+    n_same = request_span<D>(a, 0).n + kFPad;
     W = n_same * a.B * a.Hkv;
   }
   const uint32_t nb = min((W + kFMinStages - 1) / kFMinStages, gridDim.x);
@@ -311,8 +326,8 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
   const Cut cut(W, nb);
   const uint32_t w0 = cut.first(k);
   const int share = static_cast<int>(cut.first(k + 1) - w0);
-  // the place on the axis: unit (b, h), whose first stage is `start` stages
-  // after the share's first one
+  // the place on the axis: unit (b, h), whose first stage (past its padding)
+  // is `start` stages after the share's first one
   int b, h, start;
   Span p;
   {
@@ -326,8 +341,8 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
       b = lo * per;
       first = s_pre[lo];
       p = request_span<D>(a, b);
-      while (first + p.n * a.Hkv <= w0) {
-        first += p.n * a.Hkv;
+      while (first + (p.n + kFPad) * a.Hkv <= w0) {
+        first += (p.n + kFPad) * a.Hkv;
         p = request_span<D>(a, ++b);
       }
     } else {
@@ -335,13 +350,28 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
       first = b * n_same * a.Hkv;
       p = request_span<D>(a, b);
     }
-    h = (w0 - first) / p.n;
-    start = static_cast<int>(first + h * p.n) - static_cast<int>(w0);
+    h = (w0 - first) / (p.n + kFPad);
+    start = static_cast<int>(first + h * (p.n + kFPad)) - static_cast<int>(w0) + kFPad;
   }
 
   // ---- the warp's copies run ahead of its work: stage is of unit (ib, ih),
   //      at isrc if it is below ifast (stages of NR records, one after the
   //      other)
+  // bf16 query words of this lane: its tile column's head, D / 4 channels from
+  // i4 * D / 4 (requested before the copies, which fill the memory's queues)
+  uint32_t qf[2 * KT];
+  float kup;
+  auto load_q = [&](int b, int h) {
+    const int head = HALF ? (row & 3) : row;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.Hq + h * a.g + head) * D + i4 * (D / 4));
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+      const uint4 v = head < a.g ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+      qf[4 * x] = v.x, qf[4 * x + 1] = v.y, qf[4 * x + 2] = v.z, qf[4 * x + 3] = v.w;
+    }
+    kup = fp4::two_to(a.k_exp, h, 1);
+  };
+  load_q(b, h);
   const int64_t unit_bytes = a.T_cap / fp4::kTok * R::BYTES;
   int ib = b, ih = h, istart = start, is = max(0, -start) + warp, ifast = 0, islot = 0;
   const uint8_t* isrc = nullptr;
@@ -364,7 +394,7 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
           }
           is += kFWarps;
         } else {
-          istart += ip.n;
+          istart += ip.n + kFPad;
           is = warp;
           ifast = 0;
           if (++ih == a.Hkv) ih = 0, ++ib;
@@ -396,21 +426,12 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
     const int s0 = max(0, -start), end = min(p.n, share - start);
     const int unit = b * a.Hkv + h;
     // ---- query fragments: lane's head = its tile column, channels 4 i4 .. of each k-step
-    uint32_t qf[2 * KT];
     float sc0, sc1;
     {
-      const int head = HALF ? (row & 3) : row;
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(b) * a.Hq + h * a.g + head) * D + i4 * (D / 4));
-      uint32_t w[D / 8];
       float big = 0.f;
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
-        const uint4 v = head < a.g ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
-        w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
-      }
-#pragma unroll
       for (int x = 0; x < D / 8; ++x) {
-        const float2 f = unpack_bf2(w[x]);
+        const float2 f = unpack_bf2(qf[x]);
         big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
       }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
@@ -420,11 +441,11 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
       const float up = __int_as_float((127 - e) << 23);
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) {
-        const float2 f = unpack_bf2(w[x]);
+        const float2 f = unpack_bf2(qf[x]);
         qf[x] = pack_h2(f.x * up, f.y * up);
       }
       // floor: -inf (a masked score) times the factor stays -inf
-      const float sc = fmaxf(a.scale_log2 * fp4::two_to(a.k_exp, h, 1) * __int_as_float((127 + e) << 23), 1e-37f);
+      const float sc = fmaxf(a.scale_log2 * kup * __int_as_float((127 + e) << 23), 1e-37f);
       sc0 = __shfl_sync(0xffffffffu, sc, 8 * i4);
       sc1 = __shfl_sync(0xffffffffu, sc, 8 * i4 + 4);
     }
@@ -589,6 +610,8 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
       issue_next();
     }
 
+    if (start + p.n + kFPad < share) load_q(h + 1 < a.Hkv ? b : b + 1, h + 1 < a.Hkv ? h + 1 : 0);
+
     // ---- the warp's state, then the block's result for this unit: output
     //      rows, or a partial
 #pragma unroll
@@ -621,7 +644,7 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
       const float f = m == -INFINITY ? 0.f : ex2(m - M);
       const float L = warp_sum(lane < kFWarps ? f * s_ml[lane][warp][1] : 0.f);
       if (lane < kFWarps) s_f[lane][warp] = f;
-      if (lane == 0) s_tot[warp][0] = M, s_tot[warp][1] = L;
+      if (lane == 0) s_tot[0][warp][0] = M, s_tot[0][warp][1] = L;
     }
     __syncthreads();
     const bool whole = start >= 0 && end == p.n;
@@ -635,21 +658,21 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
         v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
       }
       if (whole) {
-        store_row<D>(a, b, h, hd, pos, v, s_tot[hd]);
+        store_row<D>(a, b, h, hd, pos, v, s_tot[0][hd]);
       } else {
-        const int64_t at = (2 * static_cast<int64_t>(k) + (start > 0 ? 1 : 0)) * a.g + hd;
+        const int64_t at = (2 * static_cast<int64_t>(k) + (start > kFPad ? 1 : 0)) * a.g + hd;
         *reinterpret_cast<float4*>(a.part_o + at * D + pos) = v;
-        if (pos == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(s_tot[hd][0], s_tot[hd][1]);
+        if (pos == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(s_tot[0][hd][0], s_tot[0][hd][1]);
       }
     }
     __syncthreads();
     if (!whole) {
-      if (start > 0)
+      if (start > kFPad)
         open[1] = unit, open_u0[1] = w0 + start, open_n[1] = p.n;
       else
         open[0] = unit, open_u0[0] = w0 + start, open_n[0] = p.n;
     }
-    start += p.n;
+    start += p.n + kFPad;
     if (++h == a.Hkv) {
       h = 0;
       if (start < share) p = request_span<D>(a, ++b);
@@ -661,26 +684,26 @@ __global__ void __launch_bounds__(kFThreads, 1) draft_fp4_kernel(FArgs a) {
 
   // ---- the block that finishes a unit's last partial merges them
   if (open[0] < 0 && open[1] < 0) return;
-  if (tid == 0) {  // the barrier above ordered the other threads' stores before this fence
-    __threadfence();
-    uint32_t t[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (open[i] >= 0) t[i] = atomicAdd(a.tickets + open[i], 1u);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s_last[i] = open[i] >= 0 && t[i] == cut.share_of(open_u0[i] + open_n[i] - 1) - cut.share_of(open_u0[i]);
-      if (s_last[i]) {
-        a.tickets[open[i]] = 0;
+  if (tid < 2) {  // (the barrier above ordered the other threads' stores before the fence)
+    const int u = tid ? open[1] : open[0];
+    bool last = false;
+    if (u >= 0) {
+      const uint32_t u0 = tid ? open_u0[1] : open_u0[0];
+      const uint32_t others = cut.share_of(u0 + (tid ? open_n[1] : open_n[0]) - 1) - cut.share_of(u0);
+      __threadfence();
+      last = atomicAdd(a.tickets + u, 1u) == others;
+      if (last) {
+        a.tickets[u] = 0;
         __threadfence();
       }
     }
+    s_last[tid] = last;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i)
-    if (s_last[i]) merge_unit<D, C::ML_B>(a, cut, i ? open[1] : open[0], i ? open_u0[1] : open_u0[0], i ? open_n[1] : open_n[0],
-                                 smem, s_tot);
+  const int half = tid / kFHalf;
+  if (s_last[half])
+    merge_unit<D>(a, cut, half ? open[1] : open[0], half ? open_u0[1] : open_u0[0], half ? open_n[1] : open_n[0], half,
+                  tid - half * kFHalf, smem + half * kFMergeB, s_tot[half]);
 }
 
 vc_status check_draft(const vc_attn_shape* sh, const vc_fp4_cache* c, const char* who) {
@@ -780,7 +803,7 @@ vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cach
   // blocks for the most stages that the requests can have; the kernel leaves
   // out those that their real lengths do not fill
   const vc::Span sp = vc::make_span(static_cast<uint32_t>(cache->lens ? cache->T_cap : cache->T), a.window, a.n_sink, 256 / shape->D);
-  const int64_t stages = (static_cast<int64_t>(sp.n) + 1) * shape->B * shape->Hkv;
+  const int64_t stages = (static_cast<int64_t>(sp.n) + 1 + vc::kFPad) * shape->B * shape->Hkv;
   const int blocks = static_cast<int>(
       std::min<int64_t>(p.max_blocks, (stages + vc::kFMinStages - 1) / vc::kFMinStages));
   cudaStream_t s = static_cast<cudaStream_t>(stream);

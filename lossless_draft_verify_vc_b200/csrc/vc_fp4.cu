@@ -12,6 +12,8 @@
 namespace vc {
 namespace {
 
+__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
 // Where request b's rows go: false (and a flag) when they do not fit.
 __device__ __forceinline__ bool fp4_span(const int32_t* pos, int64_t pos0, const int32_t* counts, int b, int64_t n,
                                          int64_t T_cap, uint32_t* flags, bool report, int64_t& p, int64_t& c) {
@@ -22,6 +24,36 @@ __device__ __forceinline__ bool fp4_span(const int32_t* pos, int64_t pos0, const
   return false;
 }
 
+// 32 bytes of a row: one access (whole sectors) when the rows are 32-byte
+// aligned (`wide`), else two of 16.
+struct W8 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ W8 load32(const void* p, bool wide) {
+  W8 x;
+  if (wide) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]),
+                   "=r"(x.w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+    x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
+    x.w[4] = b.x, x.w[5] = b.y, x.w[6] = b.z, x.w[7] = b.w;
+  }
+  return x;
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if constexpr (std::is_same<T, __half>::value)
@@ -30,115 +62,253 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return unpack_bf2(w);
 }
 
-// One thread per (row, K or V, block of 16 channels).
-template <int D, typename T>
-__global__ void __launch_bounds__(256) fp4_write_kernel(uint8_t* __restrict__ records, int64_t T_cap,
-                                                        const T* __restrict__ k, const T* __restrict__ v, int64_t n,
-                                                        const int32_t* __restrict__ pos, int64_t pos0,
-                                                        const int32_t* __restrict__ counts,
-                                                        const int32_t* __restrict__ k_exp,
-                                                        const int32_t* __restrict__ v_exp, int Hkv, uint32_t* flags) {
-  using R = fp4::Rec<D>;
-  const int unit = blockIdx.y;
-  const int b = unit / Hkv, h = unit - b * Hkv;
-  int64_t p, c;
-  if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c)) return;
-  const int64_t work = c * 2 * R::BLKS;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < work;
-       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int j = static_cast<int>(e % R::BLKS);
-    const bool val = (e / R::BLKS) & 1;
-    const int64_t i = e / (2 * R::BLKS);
-    const uint4* src = reinterpret_cast<const uint4*>((val ? v : k) + (static_cast<int64_t>(unit) * n + i) * D + j * 16);
-    const uint4 w0 = src[0], w1 = src[1];
-    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-    const float down = fp4::two_to(val ? v_exp : k_exp, h, -1);
-    float x[16];
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const float2 f = unpack2<T>(w[m]);
-      x[2 * m] = f.x * down;
-      x[2 * m + 1] = f.y * down;
-    }
-    uint32_t codes[2];
-    uint8_t s8;
-    if (fp4::quantise_block(x, codes, s8)) atomicOr(flags, VC_FLAG_RANGE);
-    const int64_t at = p + i;
-    const int t = static_cast<int>(at & (fp4::kTok - 1));
-    uint8_t* rec = records + (static_cast<int64_t>(unit) * (T_cap / fp4::kTok) + at / fp4::kTok) * R::BYTES;
-    if (val) {
-      *reinterpret_cast<uint32_t*>(rec + R::v_word(t, j, 0)) = codes[0];
-      *reinterpret_cast<uint32_t*>(rec + R::v_word(t, j, 1)) = codes[1];
-      rec[R::v_scale(t, j)] = s8;
-    } else {
-      *reinterpret_cast<uint2*>(rec + R::k_codes(t, j)) = make_uint2(codes[0], codes[1]);
-      rec[R::k_scale(t, j)] = s8;
-    }
-  }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
-template <typename T>
-__device__ __forceinline__ void store16(T* dst, const float (&x)[16]) {
-  if constexpr (std::is_same<T, float>::value) {
+// Values of NW words and their largest |x| * down.  Patterns of |x| are
+// ordered as integers, NaN above infinity above the rest; a run with NaN (0
+// instead) or values past the scales' range (clamped to it) is flagged.
+template <typename T, int NW>
+__device__ __forceinline__ float take(const uint32_t* w, float (&x)[2 * NW], float down, bool& odd) {
+  uint32_t m = w[0] & 0x7fff7fffu;
 #pragma unroll
-    for (int i = 0; i < 16; i += 4)
-      *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-  } else {
-    uint32_t w[8];
+  for (int i = 1; i < NW; ++i) m = max_u16x2(m, w[i] & 0x7fff7fffu);
+  m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i] = std::is_same<T, __half>::value ? pack_h2(x[2 * i], x[2 * i + 1]) : pack_bf2(x[2 * i], x[2 * i + 1]);
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  for (int i = 0; i < NW; ++i) {
+    const float2 f = unpack2<T>(w[i]);
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
   }
+  float amax = unpack2<T>(m).x * down;
+  if (!(amax <= fp4::kMaxAbs)) {
+    odd = true;
+    amax = 0.f;
+    const float lim = fp4::kMaxAbs / down;
+#pragma unroll
+    for (int i = 0; i < 2 * NW; ++i) {
+      x[i] = x[i] != x[i] ? 0.f : fminf(fmaxf(x[i], -lim), lim);
+      amax = fmaxf(amax, fabsf(x[i]));
+    }
+    amax *= down;
+  }
+  return amax;
 }
 
+constexpr int kRowWarps = 4;  // warps per block of the two kernels below
+
+// The tokens of a warp, half a record (tokens 8 half .. 8 half + 7): token t
+// of the half is row row0 + t of the call if t0 <= t < t1.
+constexpr int kHalfTok = fp4::kTok / 2;
+struct HalfRows {
+  int64_t row0;
+  int t0, t1, half;
+};
+
+__device__ __forceinline__ HalfRows half_rows(int64_t hr, int64_t p, int64_t c) {
+  HalfRows r;
+  r.row0 = hr * kHalfTok - p;
+  r.t0 = r.row0 < 0 ? static_cast<int>(-r.row0) : 0;
+  r.t1 = static_cast<int>(min(static_cast<int64_t>(kHalfTok), c - r.row0));
+  r.half = static_cast<int>(hr & 1);
+  return r;
+}
+
+// Rows into the cache, one warp per half record at a time.  A lane takes the
+// runs of the rows whose codes are contiguous in the record (the draft
+// kernel's order): of K, token lane / 4, a quarter of the channels; of V,
+// two tokens and an eighth of the channels (8 channels, D = 64: two lanes
+// share a block of 16).  Bytes of tokens that the call does not write stay.
+//
+// Bound by HBM (4 D bytes in, 18 D / 16 out per token).
 template <int D, typename T>
-__global__ void __launch_bounds__(256) fp4_read_kernel(const uint8_t* __restrict__ records, int64_t T_cap,
-                                                       T* __restrict__ k, T* __restrict__ v, int64_t n,
-                                                       const int32_t* __restrict__ pos, int64_t pos0,
-                                                       const int32_t* __restrict__ counts,
-                                                       const int32_t* __restrict__ k_exp,
-                                                       const int32_t* __restrict__ v_exp, int Hkv, uint32_t* flags) {
+__global__ void __launch_bounds__(kRowWarps * 32) fp4_write_kernel(
+    uint8_t* __restrict__ records, int64_t T_cap, const T* __restrict__ k, const T* __restrict__ v, int64_t n,
+    const int32_t* __restrict__ pos, int64_t pos0, const int32_t* __restrict__ counts,
+    const int32_t* __restrict__ k_exp, const int32_t* __restrict__ v_exp, int Hkv, uint32_t* flags) {
   using R = fp4::Rec<D>;
-  const int unit = blockIdx.y;
+  constexpr int KB = D / 64;  // 16-channel blocks of a lane's K run
+  constexpr int VW = D / 16;  // words of a lane's V run (16 or 8 channels)
+  const int unit = blockIdx.y, lane = threadIdx.x & 31;
   const int b = unit / Hkv, h = unit - b * Hkv;
   int64_t p, c;
-  if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c)) return;
-  const int64_t work = c * 2 * R::BLKS;
-  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < work;
-       e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int j = static_cast<int>(e % R::BLKS);
-    const bool val = (e / R::BLKS) & 1;
-    const int64_t i = e / (2 * R::BLKS);
-    const int64_t at = p + i;
-    const int t = static_cast<int>(at & (fp4::kTok - 1));
-    const uint8_t* rec = records + (static_cast<int64_t>(unit) * (T_cap / fp4::kTok) + at / fp4::kTok) * R::BYTES;
-    uint32_t w[2];
-    uint8_t s8;
-    if (val) {
-      w[0] = *reinterpret_cast<const uint32_t*>(rec + R::v_word(t, j, 0));
-      w[1] = *reinterpret_cast<const uint32_t*>(rec + R::v_word(t, j, 1));
-      s8 = rec[R::v_scale(t, j)];
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(rec + R::k_codes(t, j));
-      w[0] = u.x, w[1] = u.y;
-      s8 = rec[R::k_scale(t, j)];
+  if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
+  const bool kwide = aligned32(k), vwide = aligned32(v);
+  const float kdown = fp4::two_to(k_exp, h, -1), vdown = fp4::two_to(v_exp, h, -1);
+  const int64_t last = (p + c - 1) / kHalfTok;
+  const int kt = lane >> 2, vt = 2 * (lane & 3);
+  bool odd = false;
+#pragma unroll 1
+  for (int64_t hr = p / kHalfTok + blockIdx.x * kRowWarps + threadIdx.x / 32; hr <= last;
+       hr += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+    const HalfRows rr = half_rows(hr, p, c);
+    const int64_t base = (static_cast<int64_t>(unit) * n + rr.row0) * D;
+    uint8_t* dst = records + (static_cast<int64_t>(unit) * (T_cap / fp4::kTok) + hr / 2) * R::BYTES;
+    const bool klive = kt >= rr.t0 && kt < rr.t1;
+    W8 kw[KB];
+    uint32_t vw[2][VW];
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      kw[j] = W8{};
+      if (klive) kw[j] = load32(k + base + kt * D + (lane & 3) * (16 * KB) + 16 * j, kwide);
     }
-    const float up = fp4::scale_to_float(s8) * fp4::two_to(val ? v_exp : k_exp, h, 1);
-    float x[16];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      uint32_t o[4];
-      fp4::codes_to_h2(w[m], o);
+    for (int x = 0; x < 2; ++x) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 f = unpack_h2(o[q]);
-        x[8 * m + 2 * q] = f.x * up;
-        x[8 * m + 2 * q + 1] = f.y * up;
+      for (int j = 0; j < VW; ++j) vw[x][j] = 0;
+      if (vt + x >= rr.t0 && vt + x < rr.t1) {
+        const T* src = v + base + (vt + x) * D + (lane >> 2) * (D / 8);
+        if constexpr (D == 128) {
+          const W8 w = load32(src, vwide);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) vw[x][j] = w.w[j];
+        } else {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+          vw[x][0] = w.x, vw[x][1] = w.y, vw[x][2] = w.z, vw[x][3] = w.w;
+        }
       }
     }
-    store16((val ? v : k) + (static_cast<int64_t>(unit) * n + i) * D + j * 16, x);
+    // ---- K
+    uint32_t kc[2 * KB], ks = 0;
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      float f[16];
+      uint32_t cd[2];
+      const float amax = take<T, 8>(kw[j].w, f, kdown, odd);
+      const uint8_t s8 = fp4::block_scale(amax);
+      fp4::quantise_codes<16>(f, s8, kdown, cd);
+      kc[2 * j] = cd[0], kc[2 * j + 1] = cd[1];
+      ks |= static_cast<uint32_t>(s8) << (8 * j);
+    }
+    if (klive) {
+      uint8_t* at = dst + rr.half * (kHalfTok * D / 2) + lane * (8 * KB);
+      uint8_t* sc = dst + R::KS + lane * (2 * KB) + rr.half * KB;
+      if constexpr (KB == 2) {
+        *reinterpret_cast<uint4*>(at) = make_uint4(kc[0], kc[1], kc[2], kc[3]);
+        *reinterpret_cast<uint16_t*>(sc) = static_cast<uint16_t>(ks);
+      } else {
+        *reinterpret_cast<uint2*>(at) = make_uint2(kc[0], kc[1]);
+        *sc = static_cast<uint8_t>(ks);
+      }
+    }
+    // ---- V
+    uint32_t vc[2][VW / 4], vs = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float f[2 * VW];
+      float amax = take<T, VW>(vw[x], f, vdown, odd);
+      if constexpr (D == 64) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+      const uint8_t s8 = fp4::block_scale(amax);
+      fp4::quantise_codes<2 * VW>(f, s8, vdown, vc[x]);
+      vs |= static_cast<uint32_t>(s8) << (8 * x);
+    }
+    uint8_t* at = dst + R::V + lane * 16 + rr.half * (D == 128 ? 512 : 8);
+    uint8_t* sc = dst + R::VS + (D == 128 ? lane * 4 : (lane >> 3) * 16 + (lane & 3) * 4) + rr.half * 2;
+    const bool put = D == 128 || (lane & 4) == 0;  // of the two lanes that share a scale
+    if (vt >= rr.t0 && vt + 1 < rr.t1) {
+      if constexpr (D == 128)
+        *reinterpret_cast<uint4*>(at) = make_uint4(vc[0][0], vc[0][1], vc[1][0], vc[1][1]);
+      else
+        *reinterpret_cast<uint2*>(at) = make_uint2(vc[0][0], vc[1][0]);
+      if (put) *reinterpret_cast<uint16_t*>(sc) = static_cast<uint16_t>(vs);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (vt + x >= rr.t0 && vt + x < rr.t1) {
+          if constexpr (D == 128)
+            *reinterpret_cast<uint2*>(at + x * 8) = make_uint2(vc[x][0], vc[x][1]);
+          else
+            *reinterpret_cast<uint32_t*>(at + x * 4) = vc[x][0];
+          if (put) sc[x] = static_cast<uint8_t>(vs >> (8 * x));
+        }
+    }
+  }
+  if (odd) atomicOr(flags, VC_FLAG_RANGE);
+}
+
+// N values (codes of N / 8 words times `up`) to dst.
+template <int N, typename T>
+__device__ __forceinline__ void put_values(T* dst, const uint32_t* codes, float up, bool wide) {
+  float x[N];
+#pragma unroll
+  for (int m = 0; m < N / 8; ++m) {
+    uint32_t o[4];
+    fp4::codes_to_h2(codes[m], o);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 f = unpack_h2(o[q]);
+      x[8 * m + 2 * q] = f.x * up;
+      x[8 * m + 2 * q + 1] = f.y * up;
+    }
+  }
+  if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) store32(dst + i, reinterpret_cast<const uint32_t*>(x + i), wide);
+  } else {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      w[i] = std::is_same<T, __half>::value ? pack_h2(x[2 * i], x[2 * i + 1]) : pack_bf2(x[2 * i], x[2 * i + 1]);
+    if constexpr (N == 16)
+      store32(dst, w, wide);
+    else
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The way back, in the same order.  Bound by HBM.
+template <int D, typename T>
+__global__ void __launch_bounds__(kRowWarps * 32) fp4_read_kernel(
+    const uint8_t* __restrict__ records, int64_t T_cap, T* __restrict__ k, T* __restrict__ v, int64_t n,
+    const int32_t* __restrict__ pos, int64_t pos0, const int32_t* __restrict__ counts,
+    const int32_t* __restrict__ k_exp, const int32_t* __restrict__ v_exp, int Hkv, uint32_t* flags) {
+  using R = fp4::Rec<D>;
+  constexpr int KB = D / 64;
+  constexpr int VN = D / 8;  // channels of a lane's V run
+  const int unit = blockIdx.y, lane = threadIdx.x & 31;
+  const int b = unit / Hkv, h = unit - b * Hkv;
+  int64_t p, c;
+  if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
+  const bool kwide = aligned32(k), vwide = aligned32(v);
+  const float kup = fp4::two_to(k_exp, h, 1), vup = fp4::two_to(v_exp, h, 1);
+  const int64_t last = (p + c - 1) / kHalfTok;
+  const int kt = lane >> 2, vt = 2 * (lane & 3);
+#pragma unroll 1
+  for (int64_t hr = p / kHalfTok + blockIdx.x * kRowWarps + threadIdx.x / 32; hr <= last;
+       hr += static_cast<int64_t>(gridDim.x) * kRowWarps) {
+    const HalfRows rr = half_rows(hr, p, c);
+    const int64_t base = (static_cast<int64_t>(unit) * n + rr.row0) * D;
+    const uint8_t* src = records + (static_cast<int64_t>(unit) * (T_cap / fp4::kTok) + hr / 2) * R::BYTES;
+    uint32_t kc[2 * KB], vc[2][VN / 8];
+    const uint8_t* kat = src + rr.half * (kHalfTok * D / 2) + lane * (8 * KB);
+    const uint8_t* vat = src + R::V + lane * 16 + rr.half * (D == 128 ? 512 : 8);
+    const uint8_t* ksat = src + R::KS + lane * (2 * KB) + rr.half * KB;
+    const uint32_t vs = __ldg(reinterpret_cast<const uint16_t*>(
+        src + R::VS + (D == 128 ? lane * 4 : (lane >> 3) * 16 + (lane & 3) * 4) + rr.half * 2));
+    uint32_t ks;
+    if constexpr (D == 128) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(kat)), e = __ldg(reinterpret_cast<const uint4*>(vat));
+      ks = __ldg(reinterpret_cast<const uint16_t*>(ksat));
+      kc[0] = a.x, kc[1] = a.y, kc[2] = a.z, kc[3] = a.w;
+      vc[0][0] = e.x, vc[0][1] = e.y, vc[1][0] = e.z, vc[1][1] = e.w;
+    } else {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(kat)), e = __ldg(reinterpret_cast<const uint2*>(vat));
+      ks = __ldg(ksat);
+      kc[0] = a.x, kc[1] = a.y;
+      vc[0][0] = e.x, vc[1][0] = e.y;
+    }
+    if (kt >= rr.t0 && kt < rr.t1)
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        put_values<16>(k + base + kt * D + (lane & 3) * (16 * KB) + 16 * j, kc + 2 * j,
+                       fp4::scale_to_float(static_cast<uint8_t>(ks >> (8 * j))) * kup, kwide);
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (vt + x >= rr.t0 && vt + x < rr.t1)
+        put_values<VN>(v + base + (vt + x) * D + (lane >> 2) * VN, vc[x],
+                       fp4::scale_to_float(static_cast<uint8_t>(vs >> (8 * x))) * vup, vwide);
   }
 }
 
@@ -163,10 +333,11 @@ vc_status check_rows(const vc_attn_shape* shape, const vc_fp4_cache* cache, cons
   return VC_OK;
 }
 
-// Blocks of 256 threads per (request, KV head): all of the rows' blocks, at
-// most about 16 waves of the card.
-unsigned row_blocks(int64_t n, int D, int64_t units) {
-  const int64_t want = (n * 2 * (D / fp4::kBlk) + 255) / 256;
+// Blocks per (request, KV head): a warp for each half record that n rows can
+// touch, at most about 8 waves of the card.
+unsigned row_blocks(int64_t n, int64_t units) {
+  const int64_t halves = (n + kHalfTok - 2) / kHalfTok + 1;
+  const int64_t want = (halves + kRowWarps - 1) / kRowWarps;
   const int64_t most = std::max<int64_t>(1, static_cast<int64_t>(sm_count()) * 8 * 16 / units);
   return static_cast<unsigned>(std::min(want, most));
 }
@@ -186,11 +357,11 @@ vc_status vc_fp4_cache_write(const vc_attn_shape* shape, const vc_fp4_cache* cac
     return VC_OK;
   }
   const int units = shape->B * shape->Hkv;
-  const dim3 grid(vc::row_blocks(n, shape->D, units), units);
+  const dim3 grid(vc::row_blocks(n, units), units);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto go = [&](auto DD, auto tag) {
     using T = decltype(tag);
-    vc::fp4_write_kernel<decltype(DD)::value, T><<<grid, 256, 0, s>>>(
+    vc::fp4_write_kernel<decltype(DD)::value, T><<<grid, vc::kRowWarps * 32, 0, s>>>(
         static_cast<uint8_t*>(cache->records), cache->T_cap, static_cast<const T*>(k), static_cast<const T*>(v), n,
         pos, pos0, counts, cache->k_exp, cache->v_exp, shape->Hkv, static_cast<uint32_t*>(ws));
   };
@@ -213,11 +384,11 @@ vc_status vc_fp4_cache_read(const vc_attn_shape* shape, const vc_fp4_cache* cach
     return VC_OK;
   }
   const int units = shape->B * shape->Hkv;
-  const dim3 grid(vc::row_blocks(n, shape->D, units), units);
+  const dim3 grid(vc::row_blocks(n, units), units);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto go = [&](auto DD, auto tag) {
     using T = decltype(tag);
-    vc::fp4_read_kernel<decltype(DD)::value, T><<<grid, 256, 0, s>>>(
+    vc::fp4_read_kernel<decltype(DD)::value, T><<<grid, vc::kRowWarps * 32, 0, s>>>(
         static_cast<const uint8_t*>(cache->records), cache->T_cap, static_cast<T*>(k_out), static_cast<T*>(v_out), n,
         pos, pos0, counts, cache->k_exp, cache->v_exp, shape->Hkv, static_cast<uint32_t*>(ws));
   };

@@ -18,20 +18,6 @@ struct Rec {
   static constexpr int KS = 16 * D;  // key scales
   static constexpr int VS = 17 * D;  // value scales
   static constexpr int BLKS = D / kBlk;
-  // Offsets for token t of the record and 16-channel block j; a block's key
-  // codes are 8 contiguous bytes, its value codes two 4-byte words of 8
-  // channels each (contiguous when D == 128).
-  __host__ __device__ static constexpr int k_codes(int t, int j) { return t * (D / 2) + j * 8; }
-  __host__ __device__ static constexpr int v_word(int t, int j, int half) {
-    return D == 128 ? V + (t >> 3) * 512 + j * 64 + ((t & 7) >> 1) * 16 + (t & 1) * 8 + half * 4
-                    : V + (2 * j + half) * 64 + ((t & 7) >> 1) * 16 + (t >> 3) * 8 + (t & 1) * 4;
-  }
-  __host__ __device__ static constexpr int k_scale(int t, int j) {
-    return D == 128 ? KS + (t & 7) * 16 + (j >> 1) * 4 + (t >> 3) * 2 + (j & 1) : KS + (t & 7) * 8 + j * 2 + (t >> 3);
-  }
-  __host__ __device__ static constexpr int v_scale(int t, int j) {
-    return VS + j * 16 + ((t & 7) >> 1) * 4 + (t >> 3) * 2 + (t & 1);
-  }
 };
 
 // A head's power of two (clamped so that it and its inverse are normal).
@@ -93,38 +79,43 @@ __device__ __forceinline__ uint32_t floats_to_codes(const float* x) {
   return o;
 }
 
-// One block of 16 values (already multiplied by 2^-exp) -> codes and scale.
-// x / s is taken as x * (1 / s), off by at most 2^-22 of itself, and rounded
-// to 17 significant bits before the e2m1 rounding.  That decides as exact
-// division does: a border m between two codes has <= 3 significant bits, s
-// has 4 and x at most 11 (bf16, fp16), so x / s either is m, and the rounding
-// to 17 bits returns m itself, or differs from it by at least 2^-11 of m,
-// which an error of 2^-17 does not bridge.  The scale's own x / 6 is one IEEE
-// division (its borders have 5 bits, so the same argument holds).
-// Returns true when a value was NaN or outside the scales' range.
-__device__ __forceinline__ bool quantise_block(float (&x)[16], uint32_t (&codes)[2], uint8_t& s8) {
-  bool odd = false;
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const bool nan = x[i] != x[i];
-    odd |= nan;
-    x[i] = nan ? 0.f : x[i];
-    amax = fmaxf(amax, fabsf(x[i]));
-  }
-  odd |= amax > 2688.f;
-  s8 = float_to_scale(__fdiv_rn(amax, 6.f));
+// Quotients of numbers with few significant bits, as the roundings below need
+// them: x * (hi + lo) with hi + lo = 1 / d up to 2^-45 of itself is off by so
+// little that one fp32 rounding returns x / d itself where that is a number
+// of at most 20 significant bits, such as the border between two codes (e2m1:
+// 3 bits, e4m3: 5).  Any other x / d differs from a border by at least 2^-11
+// of it (x has at most 11 bits -- bf16, fp16 -- and border * d at most 8), so
+// every rounding decides as exact division does.
+struct Recip {
+  float hi, lo;
+  __device__ __forceinline__ float times(float x) const { return fmaf(x, hi, x * lo); }
+};
+__device__ __forceinline__ Recip recip(float d) {  // 1 / d; 0 for d = 0
+  Recip r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r.hi) : "f"(d));
+  r.hi = d > 0.f ? r.hi : 0.f;
+  r.lo = fmaf(-d, r.hi, 1.f) * r.hi;
+  return r;
+}
+
+constexpr float kMaxAbs = 6.f * 448.f;  // largest value in the scales' range
+
+// The scale of a block whose largest |x| * 2^-exp is amax <= kMaxAbs.
+__device__ __forceinline__ uint8_t block_scale(float amax) {
+  constexpr float hi = 1.f / 6.f, lo = static_cast<float>(1.0 / 6.0 - static_cast<double>(hi));
+  return float_to_scale(fmaf(amax, hi, amax * lo));
+}
+
+// Codes of N values x of one block under the scale s8; down: the head's 2^-exp.
+template <int N>
+__device__ __forceinline__ void quantise_codes(float (&x)[N], uint8_t s8, float down, uint32_t (&codes)[N / 8]) {
   const float s = scale_to_float(s8);
-  if (s == 0.f) {
-    codes[0] = codes[1] = 0u;
-    return odd;
-  }
-  const float r = __frcp_rn(s);
+  Recip r = recip(s);
+  r.hi *= down, r.lo *= down;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __int_as_float((__float_as_int(x[i] * r) + 0x40) & ~0x7f);
-  codes[0] = floats_to_codes(x);
-  codes[1] = floats_to_codes(x + 8);
-  return odd;
+  for (int i = 0; i < N; ++i) x[i] = r.times(x[i]);
+#pragma unroll
+  for (int i = 0; i < N / 8; ++i) codes[i] = s > 0.f ? floats_to_codes(x + 8 * i) : 0u;
 }
 
 }  // namespace fp4

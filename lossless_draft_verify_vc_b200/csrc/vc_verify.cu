@@ -54,7 +54,12 @@
 // device, and its tiles are cut into C equal chunks there.  Value rows of a
 // tile that no row sees (past the request's length, or past the first n_sink
 // keys) may hold anything: the softmax warps clear them in shared memory
-// before P.V, since 0 * NaN would reach every row.
+// before P.V, since 0 * NaN would reach every row.  Warps of a row tile without a
+// query row (one-row calls, the second row tile of g = 5) only keep step.
+// Up to 8 chunks of a unit run as one thread-block cluster and merge in it:
+// every block leaves its O rows and (m, l) in shared memory, and after a
+// cluster barrier sums its share of the rows from all of them (no partials
+// in memory, no second launch).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -109,8 +114,12 @@ struct VCfg {
   // S buffer, Q, drain; then the TMEM address slot and the abort flag
   static constexpr int NBAR = 4 * NS + 8;
   static constexpr int SMEM_B = BAR_OFF + NBAR * 8 + 16 + 1024;  // + alignment slack
+  static constexpr int ML_OFF = (BAR_OFF + NBAR * 8 + 16 + 15) / 16 * 16;  // cluster merge: (m, l) per row
+  static constexpr int ML_B = 128 * 8;
+  static constexpr int SMEM_WIN_B = ML_OFF + ML_B + 1024;
   // the partials' O boxes reuse the Q and K/V area after the tile loop
   static_assert(RTC * (D / 32) * kOBox <= BAR_OFF, "O boxes must fit below the barriers");
+  static_assert(RTC == 2 || (D / 32) * kOBox + 128 * 8 * 4 <= BAR_OFF, "merge weights fit behind them");
 };
 
 struct VArgs {
@@ -128,7 +137,33 @@ struct VArgs {
   // sliding window only
   const int32_t* lens;
   int64_t window, n_sink;
+  int cluster;  // a unit's C chunks are one cluster, which merges them
 };
+
+constexpr int kVMaxCluster = 8;  // portable cluster size
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// Address of this block's shared memory `addr` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 // Key tiles of one request under a sliding window: [0, ns) cover the first
 // n_sink keys, the others run from key w0 to key len.
@@ -267,6 +302,9 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
   // this warp's TMEM lanes and its row tile's columns
   const uint32_t lane_off = (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(wg) * kColTile;
 
+  // a warp without a query row keeps step with the others, no more
+  const bool idle = WIN && softmax_thread && (r & ~31) >= M;
+
   // row state
   const int i_row = i0 + (r < M ? r / a.g : 0);
   const int64_t vis_end = len - a.nq + i_row + 1;  // keys [0, vis_end) visible to this row
@@ -285,6 +323,23 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
         return false;
       }
     }
+  };
+
+  // WIN: value rows of tile i that no row sees (rows past T are zeros already):
+  // cleared by the softmax warps once the tile has landed, before their
+  // arrivals on bar_p; false when that wait gave up
+  auto clear_dead_values = [&](int i) -> bool {
+    const int64_t left = wt.end(first_tile + i) - wt.start(first_tile + i);
+    if (left >= kVBN || wt.end(first_tile + i) >= a.T) return true;
+    if (!wait_or_abort(&bar_v[i % NS], (i / NS) & 1)) return false;
+    unsigned char* vs = st_s + (i % NS) * C::STAGE_B + C::KV_B;
+    const int dead = static_cast<int>(left);
+    for (int e = tid; e < (kVBN - dead) * (D / 8); e += K::SOFTMAX) {
+      const int row = dead + e / (D / 8), ch = e % (D / 8);
+      *reinterpret_cast<uint4*>(vs + (ch >> 3) * (kVBN * 128) + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    return true;
   };
 
   // S = Q K^T of tile i into buffer i & 1 of every row tile: MMA thread, once
@@ -360,6 +415,22 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
       if (!fail && !wait_or_abort(&bar_s[s], (i >> 1) & 1)) fail = true;
       tc::fence_after_sync();
       bool wfail = __any_sync(FULL, fail);
+      if constexpr (WIN) {
+        if (idle) {
+          const bool bad = wfail || !clear_dead_values(i);
+          wfail = __any_sync(FULL, bad);
+          __syncwarp();
+          if ((tid & 31) == 0) {
+            if (wfail) *s_abort = 1;
+            mbar_arrive(&bar_p[s]);
+          }
+          if (wfail) {
+            fail = true;
+            break;
+          }
+          continue;
+        }
+      }
       uint32_t sr[2][32];
       if (!wfail) {
         tc::ld32(tmem + lane_off + kColS + s * kVBN, sr[0]);
@@ -424,21 +495,7 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
         }
       l_run = l_run * alpha + psum;
       if constexpr (WIN) {
-        // value rows that no row sees: cleared once the tile has landed (rows
-        // past T are zeros already), before this warp's arrival on bar_p
-        if (t_end < a.T && t_end - t0 < kVBN) {
-          if (!fail && !wait_or_abort(&bar_v[i % NS], (i / NS) & 1)) fail = true;
-          if (!fail) {
-            unsigned char* vs = st_s + (i % NS) * C::STAGE_B + C::KV_B;
-            const int dead = static_cast<int>(t_end - t0);
-            for (int e = tid; e < (kVBN - dead) * (D / 8); e += K::SOFTMAX) {
-              const int row = dead + e / (D / 8), ch = e % (D / 8);
-              *reinterpret_cast<uint4*>(vs + (ch >> 3) * (kVBN * 128) + row * 128 + (ch & 7) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-        }
+        if (!fail && !clear_dead_values(i)) fail = true;
       }
       // O is rescaled only when a row of the warp raised its maximum (rare
       // with the lazy rule); only then must the previous P.V be done first.
@@ -604,7 +661,9 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
         }
       }
       fence_proxy_async_smem();  // the boxes are read by the TMA store (async proxy)
-      if (live) {
+      if (WIN && a.cluster) {
+        *reinterpret_cast<float2*>(smem + C::ML_OFF + r * 8) = make_float2(m_out, l_out);
+      } else if (live) {
         const size_t slot = (static_cast<size_t>(unit) * a.RT + rt) * a.C + chunk;
         a.o.part_ml[(slot * rows_cap + r) * 2] = m_out;
         a.o.part_ml[(slot * rows_cap + r) * 2 + 1] = l_out;
@@ -616,6 +675,77 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
   if (warp == 0) {
     tc::fence_after_sync();
     tc::dealloc(tmem, K::TMEM_COLS);
+  }
+  if constexpr (WIN) {
+    if (a.cluster) {
+      if (!ok && softmax_thread)  // no result of this block: flagged
+        *reinterpret_cast<float2*>(smem + C::ML_OFF + r * 8) = make_float2(-INFINITY, 0.f);
+      cluster_sync();
+      // this block's share: rows chunk, chunk + C, .. of the row tile; first
+      // every chunk's weight of each (in the free second stage), then 4
+      // channels a thread, two rows' loads in flight
+      const uint32_t base = smem_addr(smem);
+      const int rows = max(0, min(a.nqt, a.nq - static_cast<int>(blockIdx.z) * a.nqt)) * a.g;
+      const int mine = rows > chunk ? (rows - chunk + a.C - 1) / a.C : 0;
+      float* w_s = reinterpret_cast<float*>(smem + (D / 32) * kOBox);
+      auto out_row = [&](int rr) {
+        const int iq = static_cast<int>(blockIdx.z) * a.nqt + rr / a.g;
+        return (static_cast<size_t>(b) * a.nq + iq) * a.Hq + h * a.g + rr % a.g;
+      };
+      if (tid < mine) {
+        const int rr = chunk + tid * a.C;
+        float2 ml[kVMaxCluster];
+        float mx = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int x = 0; x < kVMaxCluster; ++x) {
+          ml[x] = make_float2(-INFINITY, 0.f);
+          if (x < a.C) ml[x] = cluster_ld2(cluster_addr(base + C::ML_OFF + rr * 8, x));
+        }
+#pragma unroll
+        for (int x = 0; x < kVMaxCluster; ++x) mx = fmaxf(mx, ml[x].x);
+#pragma unroll
+        for (int x = 0; x < kVMaxCluster; ++x) {
+          ml[x].x = ml[x].x == -INFINITY ? 0.f : ex2(ml[x].x - mx);
+          L += ml[x].x * ml[x].y;
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+        for (int x = 0; x < kVMaxCluster; ++x) w_s[tid * kVMaxCluster + x] = ml[x].x * inv;
+        if (a.o.lse) a.o.lse[out_row(rr)] = lse_from(mx, L);
+      }
+      __syncthreads();
+      const int items = mine * (D / 4);
+#pragma unroll 1
+      for (int e = tid; e < items; e += 2 * K::THREADS) {
+        float4 o[2][kVMaxCluster];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int et = e + t * K::THREADS;
+          const int rr = chunk + et / (D / 4) * a.C, c4 = et % (D / 4);
+          const uint32_t at = base + (c4 / 8) * kOBox + rr * 128 + (((c4 & 7) ^ (rr & 7)) << 4);
+#pragma unroll
+          for (int x = 0; x < kVMaxCluster; ++x)
+            if (x < a.C && et < items) o[t][x] = cluster_ld4(cluster_addr(at, x));
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int et = e + t * K::THREADS;
+          if (et >= items) continue;
+          const int i = et / (D / 4), c4 = et % (D / 4);
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int x = 0; x < kVMaxCluster; ++x) {
+            const float w = w_s[i * kVMaxCluster + x];
+            if (x < a.C && w != 0.f)  // (the O of a chunk without keys may be anything)
+              v.x += w * o[t][x].x, v.y += w * o[t][x].y, v.z += w * o[t][x].z, v.w += w * o[t][x].w;
+          }
+          *reinterpret_cast<float4*>(a.o.out + out_row(chunk + i * a.C) * D + c4 * 4) = v;
+        }
+      }
+      __syncwarp();
+      cluster_sync();  // the others may still read this block's rows
+      return;
+    }
   }
   if (a.C > 1 && ok && tid == K::LOADER) {
 #pragma unroll 1
@@ -710,6 +840,7 @@ bool make_q_map(CUtensorMap* m, const void* base, int64_t positions, int Hq, int
 struct VPlan {
   int nqt, RT, C, tiles_per_chunk;
   int RTC;  // row tiles per block (RT when two row tiles share each K/V tile, else 1)
+  bool cluster;
   size_t off_ml, off_o, total;
 };
 
@@ -723,9 +854,10 @@ int verify_occupancy() {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (cache[dev] == 0) {
-    cudaFuncSetAttribute(verify_kernel<D, RTC, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_B);
+    const int smem = WIN ? C::SMEM_WIN_B : C::SMEM_B;
+    cudaFuncSetAttribute(verify_kernel<D, RTC, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, verify_kernel<D, RTC, WIN>, VBlk<RTC>::THREADS, C::SMEM_B) !=
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, verify_kernel<D, RTC, WIN>, VBlk<RTC>::THREADS, smem) !=
             cudaSuccess ||
         n < 1)
       n = 1;
@@ -753,15 +885,24 @@ VPlan plan_tiles(const vc_attn_shape& sh, int64_t tiles, int nq) {
   // (4 x 32K, g = 8) it is 5-8% slower -- its tile loop is bound by the
   // tensor pipe's round trips, not by HBM, so it pays off only when the
   // separate blocks' second read of K/V is what limits them.
-  p.RTC = (p.RT == 2 && units <= 16) ? 2 : 1;
-  const int occ = p.RTC == 2 ? (sh.D == 128 ? verify_occupancy<128, 2, WIN>() : verify_occupancy<64, 2, WIN>())
+  // The windowed kernel always takes one row tile per block: there a tile's
+  // warps without rows are skipped (5 of 8 warps work at g = 5) and two blocks
+  // share an SM, which is faster throughout (204 against 222 us at g = 8 and
+  // 131K keys, 154 against 170 at g = 5 and 100K, 58.5 against 69.6 at 2 x 8
+  // units, g = 5 and a window of 16000).
+  p.RTC = (!WIN && p.RT == 2 && units <= 16) ? 2 : 1;
+  const int occ = p.RTC == 2 ? (sh.D == 128 ? verify_occupancy<128, 2, false>() : verify_occupancy<64, 2, false>())
                              : (sh.D == 128 ? verify_occupancy<128, 1, WIN>() : verify_occupancy<64, 1, WIN>());
-  const int64_t slots = static_cast<int64_t>(occ) * sm_count();
+  // WIN: two blocks of one row tile fit an SM (shared memory, 256 of 512 TMEM
+  // columns) although the occupancy query answers one
+  const int64_t slots = static_cast<int64_t>(WIN ? 2 : occ) * sm_count();
   const int64_t n = static_cast<int64_t>(units) * (p.RT / p.RTC);
   int64_t c = 1, best = -1;
   for (int64_t cc = 1; cc <= tiles && cc <= 256; ++cc) {
     const int64_t waves = (n * cc + slots - 1) / slots;
-    const int64_t cost = waves * ((tiles + cc - 1) / cc + 2);
+    // WIN: a cluster's merge costs about one tile, partials and a second launch about five
+    const int64_t merge = !WIN || cc == 1 ? 0 : cc <= kVMaxCluster ? 1 : 5;
+    const int64_t cost = waves * ((tiles + cc - 1) / cc + 2) + merge;
     if (best < 0 || cost < best) {
       best = cost;
       c = cc;
@@ -770,7 +911,8 @@ VPlan plan_tiles(const vc_attn_shape& sh, int64_t tiles, int nq) {
   int64_t tpc = (tiles + c - 1) / c;
   p.tiles_per_chunk = static_cast<int>(tpc);
   p.C = static_cast<int>((tiles + tpc - 1) / tpc);
-  const int rows = p.nqt * g;
+  p.cluster = WIN && p.C > 1 && p.C <= kVMaxCluster;
+  const int rows = p.cluster ? 0 : p.nqt * g;
   const size_t nunit = static_cast<size_t>(units) * p.RT;
   p.off_ml = align_up(sizeof(WsHeader), 256);
   p.off_o = align_up(p.off_ml + nunit * p.C * rows * 2 * 4, 256);
@@ -860,31 +1002,53 @@ vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k
   a.lens = lens;
   a.window = window;
   a.n_sink = n_sink;
+  a.cluster = p.cluster;
   a.o.out = out;
   a.o.lse = lse;
   a.o.part_ml = reinterpret_cast<float*>(w + p.off_ml);
   a.o.part_o = reinterpret_cast<float*>(w + p.off_o);
   CUtensorMap to;
   memset(&to, 0, sizeof(to));
-  if (p.C > 1 && !vc::make_part_map(&to, a.o.part_o, p.nqt * a.g, shape->D, static_cast<int64_t>(units) * p.RT * p.C))
+  if (p.C > 1 && !p.cluster && !vc::make_part_map(&to, a.o.part_o, p.nqt * a.g, shape->D, static_cast<int64_t>(units) * p.RT * p.C))
     return vc::set_error(VC_ERR_CUDA, "%s: could not encode the partials' tensor map", who);
   dim3 grid(p.C, units, p.RT / p.RTC);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto go = [&](auto DD, auto RR) {
     constexpr int Dv = decltype(DD)::value, Rv = decltype(RR)::value;
     vc::verify_occupancy<Dv, Rv, WIN>();  // sets the shared-memory attribute once per device
-    vc::verify_kernel<Dv, Rv, WIN><<<grid, vc::VBlk<Rv>::THREADS, vc::VCfg<Dv, Rv>::SMEM_B, s>>>(tq, tk, tv, to, a);
+    if constexpr (WIN) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = grid;
+      cfg.blockDim = dim3(vc::VBlk<Rv>::THREADS);
+      cfg.dynamicSmemBytes = vc::VCfg<Dv, Rv>::SMEM_WIN_B;
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = p.cluster ? p.C : 1;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      cudaLaunchKernelEx(&cfg, vc::verify_kernel<Dv, Rv, WIN>, tq, tk, tv, to, a);
+    } else {
+      vc::verify_kernel<Dv, Rv, WIN><<<grid, vc::VBlk<Rv>::THREADS, vc::VCfg<Dv, Rv>::SMEM_B, s>>>(tq, tk, tv, to, a);
+    }
   };
   using I128 = std::integral_constant<int, 128>;
   using I64 = std::integral_constant<int, 64>;
   using R1 = std::integral_constant<int, 1>;
   using R2 = std::integral_constant<int, 2>;
-  if (shape->D == 128) {
-    if (p.RTC == 2) go(I128{}, R2{}); else go(I128{}, R1{});
-  } else {
-    if (p.RTC == 2) go(I64{}, R2{}); else go(I64{}, R1{});
-  }
-  if (p.C > 1) {  // chunk partials -> output rows (and lse)
+  auto by_tiles = [&](auto DD) {
+    if constexpr (WIN) {
+      go(DD, R1{});
+    } else {
+      if (p.RTC == 2) go(DD, R2{}); else go(DD, R1{});
+    }
+  };
+  if (shape->D == 128)
+    by_tiles(I128{});
+  else
+    by_tiles(I64{});
+  if (p.C > 1 && !p.cluster) {  // chunk partials -> output rows (and lse)
     const int rows_cap = p.nqt * a.g;
     const vc::VerifyRowMap map{rows_cap, p.RT, shape->Hkv, nq, p.nqt, a.g, shape->Hq, shape->D};
     const int64_t n_rows = static_cast<int64_t>(units) * p.RT * rows_cap;

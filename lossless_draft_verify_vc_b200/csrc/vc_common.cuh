@@ -248,4 +248,35 @@ __device__ __forceinline__ float warp_max_xor(float v, int lanemask) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, lanemask));
 }
 
+// A head's power of two (clamped so that it and its inverse are normal).
+__device__ __forceinline__ float two_to(const int32_t* exp, int h, int sign) {
+  if (!exp) return 1.f;
+  const int e = min(60, max(-60, __ldg(exp + h))) * sign;
+  return __int_as_float((e + 127) << 23);
+}
+
+// ---- thread-block clusters
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// Address of this block's shared memory `addr` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 }  // namespace vc

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_write_kernel(
   int64_t p, c;
   if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
   const bool kwide = aligned32(k), vwide = aligned32(v);
-  const float kdown = fp4::two_to(k_exp, h, -1), vdown = fp4::two_to(v_exp, h, -1);
+  const float kdown = two_to(k_exp, h, -1), vdown = two_to(v_exp, h, -1);
   const int64_t last = (p + c - 1) / kHalfTok;
   const int kt = lane >> 2, vt = 2 * (lane & 3);
   bool odd = false;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_read_kernel(
   int64_t p, c;
   if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
   const bool kwide = aligned32(k), vwide = aligned32(v);
-  const float kup = fp4::two_to(k_exp, h, 1), vup = fp4::two_to(v_exp, h, 1);
+  const float kup = two_to(k_exp, h, 1), vup = two_to(v_exp, h, 1);
   const int64_t last = (p + c - 1) / kHalfTok;
   const int kt = lane >> 2, vt = 2 * (lane & 3);
 #pragma unroll 1

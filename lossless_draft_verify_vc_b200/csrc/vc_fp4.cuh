@@ -20,13 +20,6 @@ struct Rec {
   static constexpr int BLKS = D / kBlk;
 };
 
-// A head's power of two (clamped so that it and its inverse are normal).
-__device__ __forceinline__ float two_to(const int32_t* exp, int h, int sign) {
-  if (!exp) return 1.f;
-  const int e = min(60, max(-60, __ldg(exp + h))) * sign;
-  return __int_as_float((e + 127) << 23);
-}
-
 // 8 e2m1 codes of a word -> 4 x f16x2 (channel pairs, exact).  Pass whole
 // words: with a byte zero-extended to a word and three of the results unused,
 // CUDA 12.9 compiled the conversion to zeros.

@@ -69,6 +69,7 @@
 
 #include "vc_splitk.cuh"
 #include "vc_tc.cuh"
+#include "vc_verify_rows.h"
 
 namespace vc {
 namespace {
@@ -141,29 +142,6 @@ struct VArgs {
 };
 
 constexpr int kVMaxCluster = 8;  // portable cluster size
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-// Address of this block's shared memory `addr` in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 
 // Key tiles of one request under a sliding window: [0, ns) cover the first
 // n_sink keys, the others run from key w0 to key len.
@@ -974,6 +952,13 @@ vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k
   VC_REQUIRE(q && k && v && out && ws, "%s: null pointer argument", who);
   VC_REQUIRE(vc::aligned16(q) && vc::aligned16(k) && vc::aligned16(v) && vc::aligned16(out) && vc::aligned16(ws),
              "%s: q, k, v, out and workspace must be 16-byte aligned", who);
+  if constexpr (WIN) {
+    if (vc::verify_rows_apply(*shape, nq)) {
+      const size_t need = vc::verify_rows_workspace(*shape, nq);
+      VC_REQUIRE(ws_bytes >= need, "%s: workspace too small (%zu < %zu)", who, ws_bytes, need);
+      return vc::verify_rows_launch(*shape, q, k, v, T, lens, nq, window, n_sink, out, lse, ws, stream);
+    }
+  }
   const vc::VPlan p =
       WIN ? vc::plan_verify_window(*shape, T, nq, window, n_sink) : vc::plan_verify(*shape, T, nq);
   VC_REQUIRE(ws_bytes >= p.total, "%s: workspace too small (%zu < %zu)", who, ws_bytes, p.total);
@@ -1087,6 +1072,7 @@ size_t vc_verify_attn_window_workspace_size(const vc_attn_shape* shape, int64_t 
     vc::set_error(VC_ERR_INVALID_ARG, "%s: need 1 <= nq <= 32, window >= 0 and n_sink >= 0", who);
     return 0;
   }
+  if (vc::verify_rows_apply(*shape, nq)) return vc::verify_rows_workspace(*shape, nq);
   return vc::plan_verify_window(*shape, T, nq, window, n_sink).total;
 }
 

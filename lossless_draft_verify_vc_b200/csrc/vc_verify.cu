@@ -143,6 +143,11 @@ struct VArgs {
 
 constexpr int kVMaxCluster = 8;  // portable cluster size
 
+// The lowest n bits (n <= 0: none, n >= 64: all).
+__device__ __forceinline__ uint64_t below(int64_t n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
 // Key tiles of one request under a sliding window: [0, ns) cover the first
 // n_sink keys, the others run from key w0 to key len.
 struct WinTiles {
@@ -431,13 +436,26 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) tmax = fmaxf(tmax, __uint_as_float(sr[c][j]));
+      } else if constexpr (WIN) {
+        // the row's live keys as bits: two instructions a score instead of six
+        const uint64_t bits = below(lim) & (below(sink) | ~below(wlo));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t m = static_cast<uint32_t>(bits >> (32 * c));
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = (m >> j & 1u) ? __uint_as_float(sr[c][j]) : -INFINITY;
+            sr[c][j] = __float_as_uint(x);
+            tmax = fmaxf(tmax, x);
+          }
+        }
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const int key = c * 32 + j;
-            const bool seen = key < lim && (!WIN || key < sink || key >= wlo);
+            const bool seen = key < lim;
             const float x = seen ? __uint_as_float(sr[c][j]) : -INFINITY;
             sr[c][j] = __float_as_uint(x);
             tmax = fmaxf(tmax, x);

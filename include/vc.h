@@ -365,7 +365,10 @@ VC_API vc_status vc_fp4_cache_read(const vc_attn_shape* shape, const vc_fp4_cach
  *   out  fp32 [B][Hq][D];  lse  fp32 [B][Hq] natural-log softmax
  *        denominators, or NULL.  L == 0: a zero row, lse -inf.
  *   window >= 0, n_sink >= 0 (without effect when window == 0).
- *   ws   workspace of vc_draft_attn_fp4_workspace_size() bytes. */
+ *   ws   workspace of vc_draft_attn_fp4_workspace_size() bytes.  Calls of
+ *        this operator and of vc_verify_attn_window, of any shapes, may use
+ *        one workspace of the largest size one after the other; one that
+ *        another entry point wrote to has to be zero-filled again. */
 VC_API size_t vc_draft_attn_fp4_workspace_size(const vc_attn_shape* shape, const vc_fp4_cache* cache);
 VC_API vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window,
                                    int64_t n_sink, const void* q, float* out, float* lse, void* ws, size_t ws_bytes,
@@ -428,7 +431,9 @@ VC_API vc_status vc_verify_attn(const vc_attn_shape* shape, const void* q, const
  *   q    bf16 [B][nq][Hq][D];  k, v  bf16 [B][Hkv][T][D]
  *   out  fp32 [B][nq][Hq][D];  lse   fp32 [B][nq][Hq] or NULL
  *   1 <= nq <= 32, 1 <= T < 2^31, window >= 0, n_sink >= 0, g = Hq / Hkv <= 8,
- *   D = 64 or 128, B * Hkv <= 65535. */
+ *   D = 64 or 128, B * Hkv <= 65535.  ws: see vc_draft_attn_fp4.
+ * A weight of the softmax is exact in fp32 for at most 8 rows per KV head
+ * (nq * g <= 8) and kept to 16 significant bits for more. */
 VC_API size_t vc_verify_attn_window_workspace_size(const vc_attn_shape* shape, int64_t T, int nq, int64_t window,
                                                    int64_t n_sink);
 VC_API vc_status vc_verify_attn_window(const vc_attn_shape* shape, const void* q, const void* k, const void* v,

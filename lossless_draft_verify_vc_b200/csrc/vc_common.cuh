@@ -44,6 +44,11 @@ struct WsHeader {
   uint32_t pad[3];
 };
 constexpr size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+// Header and a ticket for every (request, KV head): what the draft attention
+// over the 4-bit cache and the windowed verification keep at zero between
+// calls.  Their partials start behind it whatever the shape, so that calls of
+// different shapes may share a workspace.
+constexpr size_t kWsTickets = align_up(sizeof(WsHeader) + 65536 * 4, 256);
 
 // ------------------------------------------------------------- device side
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {

@@ -423,7 +423,7 @@ extern "C" {
 
 size_t vc_draft_attn_fp4_workspace_size(const vc_attn_shape* shape, const vc_fp4_cache* cache) {
   if (vc::check_draft(shape, cache, "vc_draft_attn_fp4_workspace_size") != VC_OK) return 0;
-  return vc::stream::plan(shape->B, shape->Hkv, shape->Hq / shape->Hkv, shape->D).total;
+  return vc::stream::plan(shape->Hq / shape->Hkv, shape->D).total;
 }
 
 vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window, int64_t n_sink,
@@ -435,7 +435,7 @@ vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cach
   VC_REQUIRE(vc::aligned16(cache->records) && vc::aligned16(q) && vc::aligned16(out) && vc::aligned16(ws),
              "vc_draft_attn_fp4: records, q, out and workspace must be 16-byte aligned");
   const int g = shape->Hq / shape->Hkv;
-  const vc::stream::Plan p = vc::stream::plan(shape->B, shape->Hkv, g, shape->D);
+  const vc::stream::Plan p = vc::stream::plan(g, shape->D);
   VC_REQUIRE(ws_bytes >= p.total, "vc_draft_attn_fp4: workspace too small (%zu < %zu)", ws_bytes, p.total);
   vc::FArgs a{};
   a.records = static_cast<const uint8_t*>(cache->records);

@@ -162,13 +162,15 @@ __device__ __forceinline__ void store_row(const Args& a, int b, int h, int col, 
 }
 
 // Merges the partials of one unit (first stage u0, n stages) into its output
-// rows, by T threads of the block -- all, or one half when both of its open
-// units are to be merged (t: thread among them; bar: their barrier; buf, tot:
-// their shared memory).
-constexpr int kMergeB = kMaxBlocks * 8 * 8 + kThreads * 16;
+// rows, by one half of the block: the other half may have the block's other
+// open unit to merge.  (Never by all threads: the order of the sum must not
+// depend on which block finishes last.)  t: thread of the half; bar: its
+// barrier; buf, tot: its shared memory.
+constexpr int kHalf = kThreads / 2;
+constexpr int kMergeB = kMaxBlocks * 8 * 8 + kHalf * 16;
 
 template <int D, int PAD>
-__device__ __forceinline__ void merge_unit(const Args& a, const Cut cut, int unit, uint32_t u0, int n, int bar, int T, int t,
+__device__ __forceinline__ void merge_unit(const Args& a, const Cut cut, int unit, uint32_t u0, int n, int bar, int t,
                                            unsigned char* buf, float (*tot)[2]) {
   const int warp = t >> 5, lane = t & 31;
   const int g = a.nq * a.g;  // columns
@@ -179,9 +181,9 @@ __device__ __forceinline__ void merge_unit(const Args& a, const Cut cut, int uni
   float2* ml = reinterpret_cast<float2*>(buf);  // [np][g] (m, l), then (weight, -)
   float4* sum = reinterpret_cast<float4*>(buf + kMaxBlocks * 8 * 8);
   auto at = [&](int i) { return i == 0 ? first : 2 * (static_cast<int>(kf) + i); };
-  auto sync = [&]() { asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "r"(T) : "memory"); };
+  auto sync = [&]() { asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "n"(kHalf) : "memory"); };
   // thread groups take partials in turn, 4 positions a thread, 16 loads in flight
-  const int items = g * D / 4, groups = T / items;
+  const int items = g * D / 4, groups = kHalf / items;
   const int grp = t / items, it = t - grp * items, hd = it * 4 / D;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -196,7 +198,7 @@ __device__ __forceinline__ void merge_unit(const Args& a, const Cut cut, int uni
     }
     if (base == 0) {  // meanwhile the weights
 #pragma unroll 1
-      for (int e = t; e < np * g; e += T) {
+      for (int e = t; e < np * g; e += kHalf) {
         const int i = e / g;
         ml[e] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + at(i) * g + (e - i * g));
       }
@@ -456,13 +458,10 @@ __device__ __forceinline__ void run(const Args& a, Tile& tile, unsigned char* st
     s_last[tid] = last;
   }
   __syncthreads();
-  const bool both = s_last[0] && s_last[1];
-  const int T = both ? kThreads / 2 : kThreads;
-  const int half = both ? tid / T : 0;              // which threads
-  const int u = both ? half : (s_last[0] ? 0 : 1);  // which unit
+  const int u = tid / kHalf;
   if (s_last[u])
-    merge_unit<D, PAD>(a, cut, u ? open[1] : open[0], u ? open_u0[1] : open_u0[0], u ? open_n[1] : open_n[0], 1 + half,
-                       T, tid - half * T, merge + half * kMergeB, s_tot[half]);
+    merge_unit<D, PAD>(a, cut, u ? open[1] : open[0], u ? open_u0[1] : open_u0[0], u ? open_n[1] : open_n[0], 1 + u,
+                       tid - u * kHalf, merge + u * kMergeB, s_tot[u]);
 }
 
 // ------------------------------------------------------------------ host side
@@ -472,11 +471,11 @@ struct Plan {
 };
 
 // Workspace: header, tickets, partials of every block's first and last unit.
-inline Plan plan(int B, int Hkv, int cols, int D) {
+inline Plan plan(int cols, int D) {
   Plan p;
   p.max_blocks = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
   const size_t slots = 2 * static_cast<size_t>(p.max_blocks) * cols;
-  p.off_ml = align_up(sizeof(WsHeader) + static_cast<size_t>(B) * Hkv * 4, 256);
+  p.off_ml = kWsTickets;
   p.off_o = align_up(p.off_ml + slots * 2 * 4, 256);
   p.total = align_up(p.off_o + slots * D * 4, 256);
   return p;

@@ -910,7 +910,7 @@ VPlan plan_tiles(const vc_attn_shape& sh, int64_t tiles, int nq) {
   p.cluster = WIN && p.C > 1 && p.C <= kVMaxCluster;
   const int rows = p.cluster ? 0 : p.nqt * g;
   const size_t nunit = static_cast<size_t>(units) * p.RT;
-  p.off_ml = align_up(sizeof(WsHeader), 256);
+  p.off_ml = WIN ? kWsTickets : align_up(sizeof(WsHeader), 256);
   p.off_o = align_up(p.off_ml + nunit * p.C * rows * 2 * 4, 256);
   p.total = align_up(p.off_o + nunit * p.C * rows * sh.D * 4, 256);
   return p;

@@ -259,14 +259,14 @@ void launch_rows(RArgs& a, const stream::Plan& p, cudaStream_t s) {
 }  // namespace
 
 size_t verify_rows_workspace(const vc_attn_shape& sh, int nq) {
-  return stream::plan(sh.B, sh.Hkv, nq * (sh.Hq / sh.Hkv), sh.D).total;
+  return stream::plan(nq * (sh.Hq / sh.Hkv), sh.D).total;
 }
 
 vc_status verify_rows_launch(const vc_attn_shape& sh, const void* q, const void* k, const void* v, int64_t T,
                              const int32_t* lens, int nq, int64_t window, int64_t n_sink, float* out, float* lse,
                              void* ws, void* stream_) {
   const int g = sh.Hq / sh.Hkv;
-  const stream::Plan p = stream::plan(sh.B, sh.Hkv, nq * g, sh.D);
+  const stream::Plan p = stream::plan(nq * g, sh.D);
   RArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k);

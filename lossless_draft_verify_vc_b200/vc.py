@@ -336,37 +336,49 @@ def vc_verify_attn_window(sh, q, k, v, T: int, nq: int, out, lse, ws, window: in
     _check(lib().vc_verify_attn_window(
         ctypes.byref(sh), _arg("q", q, _BF16, no * sh.D), _arg("k", k, _BF16, nk), _arg("v", v, _BF16, nk), int(T),
         _arg("lens", lens, _I32, sh.B, True), int(nq), int(window), int(n_sink), _arg("out", out, _F32, no * sh.D),
-        _arg("lse", lse, _F32, no, True), _arg("ws", ws, _U8, 0), ws.numel(), _stream(stream)))
+        _arg("lse", lse, _F32, no, True), _arg("ws", ws, _U8, 0), _size(ws), _stream(stream)))
 
 
 def _fp4_match(sh, fc):
-    if fc._dims != (sh.B, sh.Hkv, sh.D):
+    if getattr(fc, "_dims", None) not in (None, (sh.B, sh.Hkv, sh.D)):  # (a descriptor from fp4_cache)
         raise ValueError(f"the cache holds (B, Hkv, D) = {fc._dims}, the shape says {(sh.B, sh.Hkv, sh.D)}")
 
 
-def _fp4_rows(f, sh, fc, k, v, dtypes, n, ws, pos, pos0, counts, stream):
+def _size(ws) -> int:
+    return ws.numel() if hasattr(ws, "numel") else 1 << 62  # a raw pointer: the caller vouches for its size
+
+
+def _fp4_rows(f, sh, fc, k, v, dtypes, n, ws, pos, pos0, counts, dtype, stream):
     _fp4_match(sh, fc)
-    if k.dtype != v.dtype:
+    if dtype is None:
+        if isinstance(k, int) or isinstance(v, int):
+            raise ValueError("raw pointers need dtype")
+        dtype = k.dtype
+    if not isinstance(k, int) and not isinstance(v, int) and k.dtype != v.dtype:
         raise ValueError("k and v must have the same dtype")
+    if dtype not in dtypes:
+        raise ValueError(f"k and v must be {' or '.join(str(d) for d in dtypes)} (got {dtype})")
+    dtypes = (dtype,)
     size = sh.B * sh.Hkv * int(n) * sh.D
     _check(f(ctypes.byref(sh), ctypes.byref(fc), _arg("k", k, dtypes, size), _arg("v", v, dtypes, size),
-             _CODES[k.dtype], int(n), _arg("pos", pos, _I32, sh.B, True), int(pos0),
-             _arg("counts", counts, _I32, sh.B, True), _arg("ws", ws, _U8, 0), ws.numel(), _stream(stream)))
+             _CODES[dtype], int(n), _arg("pos", pos, _I32, sh.B, True), int(pos0),
+             _arg("counts", counts, _I32, sh.B, True), _arg("ws", ws, _U8, 0), _size(ws), _stream(stream)))
 
 
-def vc_fp4_cache_write(sh, fc, k, v, n: int, ws, pos=None, pos0: int = 0, counts=None, stream=None):
+def vc_fp4_cache_write(sh, fc, k, v, n: int, ws, pos=None, pos0: int = 0, counts=None, dtype=None, stream=None):
     """Quantises rows k, v (bf16 or fp16 [B, Hkv, n, D]) into tokens
     pos[b] + i, i < counts[b], of a 4-bit floating-point cache (pos, counts
-    int32 [B]; default pos0 and n for every request)."""
-    _fp4_rows(lib().vc_fp4_cache_write, sh, fc, k, v, (torch.bfloat16, torch.float16), n, ws, pos, pos0, counts,
+    int32 [B]; default pos0 and n for every request).  dtype: the rows' torch
+    dtype, for raw pointers."""
+    _fp4_rows(lib().vc_fp4_cache_write, sh, fc, k, v, (torch.bfloat16, torch.float16), n, ws, pos, pos0, counts, dtype,
               stream)
 
 
-def vc_fp4_cache_read(sh, fc, n: int, k_out, v_out, ws, pos=None, pos0: int = 0, counts=None, stream=None):
+def vc_fp4_cache_read(sh, fc, n: int, k_out, v_out, ws, pos=None, pos0: int = 0, counts=None, dtype=None, stream=None):
     """Tokens pos[b] + i, i < counts[b], of a 4-bit floating-point cache back
     to rows i of k_out, v_out (bf16, fp16 or fp32 [B, Hkv, n, D])."""
     _fp4_rows(lib().vc_fp4_cache_read, sh, fc, k_out, v_out, (torch.bfloat16, torch.float16, torch.float32), n, ws,
-              pos, pos0, counts, stream)
+              pos, pos0, counts, dtype, stream)
 
 
 def vc_draft_attn_fp4_workspace_size(sh, fc) -> int:
@@ -380,7 +392,7 @@ def vc_draft_attn_fp4(sh, fc, q, out, ws, lse=None, window: int = 0, n_sink: int
     n = sh.B * sh.Hq
     _check(lib().vc_draft_attn_fp4(ctypes.byref(sh), ctypes.byref(fc), int(window), int(n_sink),
                                    _arg("q", q, _BF16, n * sh.D), _arg("out", out, _F32, n * sh.D),
-                                   _arg("lse", lse, _F32, n, True), _arg("ws", ws, _U8, 0), ws.numel(),
+                                   _arg("lse", lse, _F32, n, True), _arg("ws", ws, _U8, 0), _size(ws),
                                    _stream(stream)))
 
 

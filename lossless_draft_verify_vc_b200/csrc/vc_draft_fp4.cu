@@ -27,9 +27,9 @@
 //
 // The split of the work, its merges and their reasons are in vc_stream.cuh;
 // every warp reads its stages through its own ring of bulk copies, which runs
-// ahead across units.  Bound by HBM: 8 x 32K tokens (302 MB) take 61 us, of
+// ahead across units.  Bound by HBM: 8 x 32K tokens (302 MB) take 59 us, of
 // which the stage loops run at 6.2 TB/s and starting, merging and uneven ends
-// take 12 us; below that instruction issue is next (about 300 instructions a
+// take 10 us; below that instruction issue is next (about 285 instructions a
 // record, 64 of them e2m1 conversions and 64 scalings).
 #include <algorithm>
 
@@ -62,6 +62,18 @@ __device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[
 // (a & m) | (b & ~m)
 __device__ __forceinline__ uint32_t blend(uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); }
 
+// One half of an f16x2 in both, and a product with it: as intrinsics, which
+// the compiler folds into the multiplication's operand.
+template <int HIGH>
+__device__ __forceinline__ __half2 both(uint32_t p) {
+  const __half2 v = *reinterpret_cast<__half2*>(&p);
+  return HIGH ? __high2half2(v) : __low2half2(v);
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, __half2 b) {
+  const __half2 v = __hmul2(*reinterpret_cast<__half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 template <int D_, bool HALF>
 struct FTile {
   static constexpr int D = D_;
@@ -75,12 +87,13 @@ struct FTile {
   static constexpr int COLS = HALF ? 4 : 8;
   static constexpr int SMEM_B = STATE_OFF + stream::kWarps * stream::State<D>::bytes(COLS);
   static_assert(2 * stream::kMergeB <= BAR_OFF, "the final merges' buffers take the rings' place");
-  // Measured on B200 (us of device time per call at 8 requests x 32K, 1 x 262K,
-  // 4 x window 4096): a unit's begin -- query load, state, partial -- costs a
-  // block about as much as 24 stages; counted as nothing the blocks that hold
-  // parts of two units finish last: 66.0, 66.4, 22.5 against 61.5, 60.4, 15.7.
-  static constexpr int PAD = 24;
-  static constexpr int MIN = 40;  // padding and a short unit (16 stages)
+  // A unit's begin -- query load, state, partial -- costs a block about as much
+  // as 32 stages; counted as nothing the blocks that hold parts of two units
+  // finish last.  Measured on B200, us of device time per call at 8 requests x
+  // 32K and 1 x 262K: 8 stages 62.5, 62.4; 24 59.7, 58.1; 32 59.2, 57.7; 40
+  // 58.9, 57.7 (but one unit of 65K 19.6 against 18.4).
+  static constexpr int PAD = 32;
+  static constexpr int MIN = 48;  // padding and a short unit (16 stages)
   static constexpr int GAIN = 40;  // see stream::choose
   static constexpr int KT = D / 16;  // k-steps of a score tile, m-tiles of the values
   using R = fp4::Rec<D>;
@@ -205,7 +218,18 @@ struct FTile {
       return false;
     const unsigned char* st = ring + slot * STAGE;
     if (++slot == NST) slot = 0, phase ^= 1;
+    // two copies of the body: the masks cost the whole stages nothing (9 of 298 instructions a record)
+    if (full)
+      body<true>(p, x, st);
+    else
+      body<false>(p, x, st);
+    __syncwarp();
+    issue_next();
+    return true;
+  }
 
+  template <bool full>
+  __device__ __forceinline__ void body(const Span& p, int x, const unsigned char* st) {
     // hi lanes keep a weight's first 11 bits, lo lanes the rest: v = p * lo_f + ((p & mask) ^ lo_s)
     const float lo_f = i4 < 2 ? 0.f : 1.f;
     const uint32_t lo_s = i4 < 2 ? 0u : 0x80000000u;
@@ -214,7 +238,8 @@ struct FTile {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const unsigned char* rec = st + r * REC;
-      uint32_t ka[D / 32], kb[D / 32], sa[D / 64], sb[D / 64];  // token row, row + 8: codes, scales (both halves)
+      uint32_t ka[D / 32], kb[D / 32];
+      __half2 sa[D / 64], sb[D / 64];  // token row, row + 8: codes, scales (both halves)
       if constexpr (D == 128) {
         const uint4 x = *reinterpret_cast<const uint4*>(rec + lane * 16);
         const uint4 y = *reinterpret_cast<const uint4*>(rec + 512 + lane * 16);
@@ -222,16 +247,16 @@ struct FTile {
         kb[0] = y.x, kb[1] = y.y, kb[2] = y.z, kb[3] = y.w;
         const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + R::KS + lane * 4);
         const uint32_t p = fp4::scales_to_h2(w & 0xffffu), q = fp4::scales_to_h2(w >> 16);
-        sa[0] = prmt(p, p, 0x1010), sa[1] = prmt(p, p, 0x3232);
-        sb[0] = prmt(q, q, 0x1010), sb[1] = prmt(q, q, 0x3232);
+        sa[0] = both<0>(p), sa[1] = both<1>(p);
+        sb[0] = both<0>(q), sb[1] = both<1>(q);
       } else {
         const uint2 x = *reinterpret_cast<const uint2*>(rec + lane * 8);
         const uint2 y = *reinterpret_cast<const uint2*>(rec + 256 + lane * 8);
         ka[0] = x.x, ka[1] = x.y;
         kb[0] = y.x, kb[1] = y.y;
         const uint32_t p = fp4::scales_to_h2(*reinterpret_cast<const uint16_t*>(rec + R::KS + lane * 2));
-        sa[0] = prmt(p, p, 0x1010);
-        sb[0] = prmt(p, p, 0x3232);
+        sa[0] = both<0>(p);
+        sb[0] = both<1>(p);
       }
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
@@ -239,7 +264,7 @@ struct FTile {
         fp4::codes_to_h2(ka[w], oa);
         fp4::codes_to_h2(kb[w], ob);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) oa[x] = hmul2(oa[x], sa[w / 2]), ob[x] = hmul2(ob[x], sb[w / 2]);
+        for (int x = 0; x < 4; ++x) oa[x] = mul_h2(oa[x], sa[w / 2]), ob[x] = mul_h2(ob[x], sb[w / 2]);
         const uint32_t f0[4] = {oa[0], ob[0], oa[1], ob[1]}, f1[4] = {oa[2], ob[2], oa[3], ob[3]};
         if (w == 0)
           mma_f16_zero(c[r], f0, qf[0], qf[1]);
@@ -349,9 +374,6 @@ struct FTile {
         }
       }
     }
-    __syncwarp();
-    issue_next();
-    return true;
   }
 
   __device__ __forceinline__ void finish(float* o, float (*ml)[2], bool failed) {

@@ -203,18 +203,22 @@ _U8 = (torch.uint8,)
 _CODES = {torch.float32: VC_F32, torch.bfloat16: VC_BF16, torch.float16: VC_F16}
 
 
-def _arg(name: str, x, dtypes, n: int, optional: bool = False) -> int:
+def _arg(name: str, x, dtypes, n: int, optional: bool = False, dev: int | None = None) -> int:
     """Device pointer of a tensor argument after checking it: contiguous, on
-    the current device, of one of `dtypes` and of at least n elements.
-    Integers (raw device pointers) pass through."""
-    if x is None:
+    the current device (dev, when the caller has looked it up), of one of
+    `dtypes` and of at least n elements.  Integers (raw device pointers) pass
+    through."""
+    try:
+        if x.dtype in dtypes and x.numel() >= n and x.is_contiguous() and 0 <= x.get_device() == (_device() if dev is None else dev):
+            return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+        if x is not None:
+            raise
         if optional:
             return 0
-        raise ValueError(f"{name} is missing")
-    if isinstance(x, int):
-        return x
-    if x.dtype in dtypes and x.numel() >= n and x.is_contiguous() and 0 <= x.get_device() == _device():
-        return x.data_ptr()
+        raise ValueError(f"{name} is missing") from None
     if x.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {x.dtype})")
     if x.numel() < n:
@@ -222,6 +226,13 @@ def _arg(name: str, x, dtypes, n: int, optional: bool = False) -> int:
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _current(x) -> int:
+    """The current device if the tensor x is on it, else -1 (which no tensor passes)."""
+    if isinstance(x, int):
+        return _device()
+    return x.get_device() if x is not None and 0 <= x.get_device() == _device() else -1
 
 
 def _stream(stream) -> int:
@@ -332,11 +343,13 @@ def vc_verify_attn_window(sh, q, k, v, T: int, nq: int, out, lse, ws, window: in
     """vc_verify_attn with a sliding window of `window` tokens (0: none), the
     first n_sink tokens visible throughout and optional per-request lengths
     (int32 [B]); see include/vc.h."""
-    nk, no = sh.B * sh.Hkv * int(T) * sh.D, sh.B * int(nq) * sh.Hq
+    B, D = sh.B, sh.D
+    nk, no, dev = B * sh.Hkv * int(T) * D, B * int(nq) * sh.Hq, _current(k)
     _check(lib().vc_verify_attn_window(
-        ctypes.byref(sh), _arg("q", q, _BF16, no * sh.D), _arg("k", k, _BF16, nk), _arg("v", v, _BF16, nk), int(T),
-        _arg("lens", lens, _I32, sh.B, True), int(nq), int(window), int(n_sink), _arg("out", out, _F32, no * sh.D),
-        _arg("lse", lse, _F32, no, True), _arg("ws", ws, _U8, 0), _size(ws), _stream(stream)))
+        ctypes.byref(sh), _arg("q", q, _BF16, no * D, False, dev), _arg("k", k, _BF16, nk, False, dev),
+        _arg("v", v, _BF16, nk, False, dev), int(T), _arg("lens", lens, _I32, B, True, dev), int(nq), int(window),
+        int(n_sink), _arg("out", out, _F32, no * D, False, dev), _arg("lse", lse, _F32, no, True, dev),
+        _arg("ws", ws, _U8, 0, False, dev), _size(ws), _stream(stream)))
 
 
 def _fp4_match(sh, fc):
@@ -359,10 +372,12 @@ def _fp4_rows(f, sh, fc, k, v, dtypes, n, ws, pos, pos0, counts, dtype, stream):
     if dtype not in dtypes:
         raise ValueError(f"k and v must be {' or '.join(str(d) for d in dtypes)} (got {dtype})")
     dtypes = (dtype,)
-    size = sh.B * sh.Hkv * int(n) * sh.D
-    _check(f(ctypes.byref(sh), ctypes.byref(fc), _arg("k", k, dtypes, size), _arg("v", v, dtypes, size),
-             _CODES[dtype], int(n), _arg("pos", pos, _I32, sh.B, True), int(pos0),
-             _arg("counts", counts, _I32, sh.B, True), _arg("ws", ws, _U8, 0), _size(ws), _stream(stream)))
+    B, dev = sh.B, _current(k)
+    size = B * sh.Hkv * int(n) * sh.D
+    _check(f(ctypes.byref(sh), ctypes.byref(fc), _arg("k", k, dtypes, size, False, dev),
+             _arg("v", v, dtypes, size, False, dev), _CODES[dtype], int(n), _arg("pos", pos, _I32, B, True, dev),
+             int(pos0), _arg("counts", counts, _I32, B, True, dev), _arg("ws", ws, _U8, 0, False, dev), _size(ws),
+             _stream(stream)))
 
 
 def vc_fp4_cache_write(sh, fc, k, v, n: int, ws, pos=None, pos0: int = 0, counts=None, dtype=None, stream=None):
@@ -389,10 +404,11 @@ def vc_draft_attn_fp4(sh, fc, q, out, ws, lse=None, window: int = 0, n_sink: int
     """Draft attention over a 4-bit floating-point cache, optionally limited
     to a sliding window and the first n_sink tokens (see include/vc.h)."""
     _fp4_match(sh, fc)
-    n = sh.B * sh.Hq
+    n, dev = sh.B * sh.Hq, _current(q)
+    size = n * sh.D
     _check(lib().vc_draft_attn_fp4(ctypes.byref(sh), ctypes.byref(fc), int(window), int(n_sink),
-                                   _arg("q", q, _BF16, n * sh.D), _arg("out", out, _F32, n * sh.D),
-                                   _arg("lse", lse, _F32, n, True), _arg("ws", ws, _U8, 0), _size(ws),
+                                   _arg("q", q, _BF16, size, False, dev), _arg("out", out, _F32, size, False, dev),
+                                   _arg("lse", lse, _F32, n, True, dev), _arg("ws", ws, _U8, 0, False, dev), _size(ws),
                                    _stream(stream)))
 
 

@@ -151,10 +151,10 @@ __device__ __forceinline__ uint64_t below(int64_t n) {
 // Key tiles of one request under a sliding window: [0, ns) cover the first
 // n_sink keys, the others run from key w0 to key len.
 struct WinTiles {
-  int64_t len, w0, n_sink;
+  int len, w0, n_sink;
   int ns, n;
-  __device__ WinTiles(int64_t len_, int nq, int64_t window, int64_t n_sink_) : len(len_), n_sink(n_sink_) {
-    w0 = window > 0 ? len - nq + 1 - window : 0;
+  __device__ WinTiles(int64_t len_, int nq, int64_t window, int64_t n_sink_) : len(static_cast<int>(len_)), n_sink(static_cast<int>(n_sink_)) {
+    w0 = window > 0 ? len - nq + 1 - static_cast<int>(window) : 0;
     if (w0 < 0) w0 = 0;
     if (n_sink >= w0) {  // one list from key 0
       w0 = 0;
@@ -164,8 +164,8 @@ struct WinTiles {
     }
     n = ns + static_cast<int>((len - w0 + kVBN - 1) / kVBN);
   }
-  __device__ int64_t start(int i) const { return i < ns ? static_cast<int64_t>(i) * kVBN : w0 + static_cast<int64_t>(i - ns) * kVBN; }
-  __device__ int64_t end(int i) const { return i < ns ? n_sink : len; }
+  __device__ int start(int i) const { return i < ns ? i * kVBN : w0 + (i - ns) * kVBN; }
+  __device__ int end(int i) const { return i < ns ? n_sink : len; }
 };
 
 template <int D, int RTC, bool WIN>
@@ -423,12 +423,14 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
 #pragma unroll
         for (int j = 0; j < 32; ++j) sr[0][j] = sr[1][j] = 0u;
       }
-      const int64_t t0 = WIN ? wt.start(first_tile + i) : k_begin + static_cast<int64_t>(i) * kVBN;
-      const int64_t t_end = WIN ? wt.end(first_tile + i) : k_end;
-      const int64_t lim = min(vis_end, t_end) - t0;  // keys [t0, t0 + lim) are live
+      // (WIN: 32-bit positions)
+      using P = typename std::conditional<WIN, int, int64_t>::type;
+      const P t0 = WIN ? static_cast<P>(wt.start(first_tile + i)) : static_cast<P>(k_begin + static_cast<int64_t>(i) * kVBN);
+      const P t_end = WIN ? static_cast<P>(wt.end(first_tile + i)) : static_cast<P>(k_end);
+      const P lim = min(static_cast<P>(vis_end), t_end) - t0;  // keys [t0, t0 + lim) are live
       // sliding window: of those, keys below t0 + sink or from t0 + wlo on
-      const int64_t sink = WIN ? a.n_sink - t0 : 0;
-      const int64_t wlo = WIN && a.window > 0 ? vis_end - a.window - t0 : 0;
+      const P sink = WIN ? static_cast<P>(a.n_sink) - t0 : 0;
+      const P wlo = WIN && a.window > 0 ? static_cast<P>(vis_end) - static_cast<P>(a.window) - t0 : 0;
       // raw scores; the scale (> 0) is applied in the exponent's FMA below
       float tmax = -INFINITY;
       if (__all_sync(FULL, lim >= kVBN && (!WIN || sink >= kVBN || wlo <= 0))) {  // whole tile visible to the warp's rows: no mask
@@ -473,6 +475,7 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
       const float m_sub = m_use == -INFINITY ? 0.f : m_use;
       uint32_t phi[32], plo[32];
       float psum = 0.f;
+      float2 ps2 = make_float2(0.f, 0.f);
       // pairs of columns in packed fp32x2 arithmetic (each half rounds as the
       // scalar instruction would)
       const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), nm2 = make_float2(-m_sub, -m_sub);
@@ -483,13 +486,16 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
         for (int j = 0; j < 32; j += 2) {
           const float2 e = __ffma2_rn(make_float2(__uint_as_float(sr[c][j]), __uint_as_float(sr[c][j + 1])), sc2, nm2);
           const float p0 = ex2(e.x), p1 = ex2(e.y);
-          psum += p0 + p1;
+          if constexpr (WIN)  // (one packed addition; the sum of even and of odd keys)
+            ps2 = __fadd2_rn(ps2, make_float2(p0, p1));
+          else
+            psum += p0 + p1;
           const uint32_t hw = pack_bf2(p0, p1);
           const float2 lo = __ffma2_rn(unpack_bf2(hw), neg1, make_float2(p0, p1));  // p - bf16(p), exact
           phi[c * 16 + j / 2] = hw;
           plo[c * 16 + j / 2] = pack_bf2(lo.x, lo.y);
         }
-      l_run = l_run * alpha + psum;
+      l_run = l_run * alpha + (WIN ? ps2.x + ps2.y : psum);
       if constexpr (WIN) {
         if (!fail && !clear_dead_values(i)) fail = true;
       }
@@ -1099,8 +1105,8 @@ vc_status vc_verify_attn_window(const vc_attn_shape* shape, const void* q, const
                                 void* ws, size_t ws_bytes, void* stream) {
   VC_REQUIRE(window >= 0 && n_sink >= 0, "vc_verify_attn_window: window and n_sink must be >= 0");
   // no position reaches 2^31: larger values mean the same and would overflow
-  window = std::min<int64_t>(window, int64_t(1) << 31);
-  n_sink = std::min<int64_t>(n_sink, int64_t(1) << 31);
+  window = window >= T ? 0 : window;
+  n_sink = std::min<int64_t>(n_sink, INT32_MAX);
   return vc::verify_launch<true>(shape, q, k, v, T, lens, nq, window, n_sink, out, lse, ws, ws_bytes, stream, -1,
                                  2000000000ull);
 }

@@ -17,13 +17,16 @@ __device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_c
 // Where request b's rows go: false (and a flag) when they do not fit.
 __device__ __forceinline__ bool fp4_span(const int32_t* pos, int64_t pos0, const int32_t* counts, int b, int64_t n,
                                          int64_t T_cap, uint32_t* flags, bool report, int64_t& p, int64_t& c) {
-  p = pos ? static_cast<int64_t>(__ldg(pos + b)) : pos0;
-  c = counts ? static_cast<int64_t>(__ldg(counts + b)) : n;
+  p = pos ? static_cast<int64_t>(__ldcg(pos + b)) : pos0;
+  c = counts ? static_cast<int64_t>(__ldcg(counts + b)) : n;
   if (p >= 0 && c >= 0 && c <= n && p + c <= T_cap) return true;
   if (report) atomicOr(flags, VC_FLAG_BAD_LENGTH);
   return false;
 }
 
+// Loads in this file avoid the read-only path: a programmatic dependent is
+// resident while the call before it still writes what it will read.
+//
 // 32 bytes of a row: one access (whole sectors) when the rows are 32-byte
 // aligned (`wide`), else two of 16.
 struct W8 {
@@ -32,12 +35,12 @@ struct W8 {
 __device__ __forceinline__ W8 load32(const void* p, bool wide) {
   W8 x;
   if (wide) {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
                  : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]),
                    "=r"(x.w[7])
                  : "l"(p));
   } else {
-    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+    const uint4 a = __ldcg(static_cast<const uint4*>(p)), b = __ldcg(static_cast<const uint4*>(p) + 1);
     x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
     x.w[4] = b.x, x.w[5] = b.y, x.w[6] = b.z, x.w[7] = b.w;
   }
@@ -133,6 +136,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_write_kernel(
   constexpr int VW = D / 16;  // words of a lane's V run (16 or 8 channels)
   const int unit = blockIdx.y, lane = threadIdx.x & 31;
   const int b = unit / Hkv, h = unit - b * Hkv;
+  // the next call's blocks may be scheduled as this grid's retire; they wait
+  // here for its end, as these do for the call before
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   int64_t p, c;
   if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
   const bool kwide = aligned32(k), vwide = aligned32(v);
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_write_kernel(
 #pragma unroll
           for (int j = 0; j < 8; ++j) vw[x][j] = w.w[j];
         } else {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+          const uint4 w = __ldcg(reinterpret_cast<const uint4*>(src));
           vw[x][0] = w.x, vw[x][1] = w.y, vw[x][2] = w.z, vw[x][3] = w.w;
         }
       }
@@ -269,6 +276,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_read_kernel(
   constexpr int VN = D / 8;  // channels of a lane's V run
   const int unit = blockIdx.y, lane = threadIdx.x & 31;
   const int b = unit / Hkv, h = unit - b * Hkv;
+  // the next call's blocks may be scheduled as this grid's retire; they wait
+  // here for its end, as these do for the call before
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   int64_t p, c;
   if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
   const bool kwide = aligned32(k), vwide = aligned32(v);
@@ -285,17 +296,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_read_kernel(
     const uint8_t* kat = src + rr.half * (kHalfTok * D / 2) + lane * (8 * KB);
     const uint8_t* vat = src + R::V + lane * 16 + rr.half * (D == 128 ? 512 : 8);
     const uint8_t* ksat = src + R::KS + lane * (2 * KB) + rr.half * KB;
-    const uint32_t vs = __ldg(reinterpret_cast<const uint16_t*>(
+    const uint32_t vs = __ldcg(reinterpret_cast<const uint16_t*>(
         src + R::VS + (D == 128 ? lane * 4 : (lane >> 3) * 16 + (lane & 3) * 4) + rr.half * 2));
     uint32_t ks;
     if constexpr (D == 128) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(kat)), e = __ldg(reinterpret_cast<const uint4*>(vat));
-      ks = __ldg(reinterpret_cast<const uint16_t*>(ksat));
+      const uint4 a = __ldcg(reinterpret_cast<const uint4*>(kat)), e = __ldcg(reinterpret_cast<const uint4*>(vat));
+      ks = __ldcg(reinterpret_cast<const uint16_t*>(ksat));
       kc[0] = a.x, kc[1] = a.y, kc[2] = a.z, kc[3] = a.w;
       vc[0][0] = e.x, vc[0][1] = e.y, vc[1][0] = e.z, vc[1][1] = e.w;
     } else {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(kat)), e = __ldg(reinterpret_cast<const uint2*>(vat));
-      ks = __ldg(ksat);
+      const uint2 a = __ldcg(reinterpret_cast<const uint2*>(kat)), e = __ldcg(reinterpret_cast<const uint2*>(vat));
+      ks = __ldcg(ksat);
       kc[0] = a.x, kc[1] = a.y;
       vc[0][0] = e.x, vc[1][0] = e.y;
     }
@@ -342,6 +353,21 @@ unsigned row_blocks(int64_t n, int64_t units) {
   return static_cast<unsigned>(std::min(want, most));
 }
 
+// Launch as a programmatic dependent.
+template <class... Params, class... Args>
+void launch_rows(void (*kernel)(Params...), dim3 grid, void* stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRowWarps * 32);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 }  // namespace
 }  // namespace vc
 
@@ -358,10 +384,9 @@ vc_status vc_fp4_cache_write(const vc_attn_shape* shape, const vc_fp4_cache* cac
   }
   const int units = shape->B * shape->Hkv;
   const dim3 grid(vc::row_blocks(n, units), units);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto go = [&](auto DD, auto tag) {
     using T = decltype(tag);
-    vc::fp4_write_kernel<decltype(DD)::value, T><<<grid, vc::kRowWarps * 32, 0, s>>>(
+    vc::launch_rows(vc::fp4_write_kernel<decltype(DD)::value, T>, grid, stream,
         static_cast<uint8_t*>(cache->records), cache->T_cap, static_cast<const T*>(k), static_cast<const T*>(v), n,
         pos, pos0, counts, cache->k_exp, cache->v_exp, shape->Hkv, static_cast<uint32_t*>(ws));
   };
@@ -385,10 +410,9 @@ vc_status vc_fp4_cache_read(const vc_attn_shape* shape, const vc_fp4_cache* cach
   }
   const int units = shape->B * shape->Hkv;
   const dim3 grid(vc::row_blocks(n, units), units);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto go = [&](auto DD, auto tag) {
     using T = decltype(tag);
-    vc::fp4_read_kernel<decltype(DD)::value, T><<<grid, vc::kRowWarps * 32, 0, s>>>(
+    vc::launch_rows(vc::fp4_read_kernel<decltype(DD)::value, T>, grid, stream,
         static_cast<const uint8_t*>(cache->records), cache->T_cap, static_cast<T*>(k_out), static_cast<T*>(v_out), n,
         pos, pos0, counts, cache->k_exp, cache->v_exp, shape->Hkv, static_cast<uint32_t*>(ws));
   };

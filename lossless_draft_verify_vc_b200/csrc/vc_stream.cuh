@@ -19,6 +19,10 @@
 // one unit's stages and merge through each other's shared memory, without the
 // axis, partials in memory and tickets.  See choose() for the rule.
 //
+// Both kernels are programmatic dependents, resident while the call before
+// them still writes: nothing is read before griddepcontrol.wait, and nothing
+// through the read-only path.
+//
 // Code outside the stage loop is kept short rather than fast: it runs once or
 // twice per block out of an empty instruction cache (unrolled merges and one
 // block of 4 warps more per SM cost 5 us of 66 at 8 x 32K tokens).
@@ -85,7 +89,7 @@ template <int NR>
 __device__ __forceinline__ Span request_span(const Args& a, int b) {
   uint32_t L = a.T;
   if (a.lens) {
-    L = static_cast<uint32_t>(__ldg(a.lens + b));
+    L = static_cast<uint32_t>(a.lens[b]);
     if (L > a.T_cap) L = 0;  // (a negative length too)
   }
   return make_span(L, a.nq, a.window, a.n_sink, NR);
@@ -273,7 +277,7 @@ __device__ __forceinline__ void run(const Args& a, Tile& tile, unsigned char* st
   if (a.cluster) {  // rank r of a unit's C blocks: stages from ceil(r n / C)
     const int unit = k / a.cluster, rank = k - unit * a.cluster;
     b = unit / a.Hkv, h = unit - b * a.Hkv;
-    if (a.lens && tid == 0 && static_cast<uint32_t>(__ldg(a.lens + b)) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
+    if (a.lens && tid == 0 && static_cast<uint32_t>(a.lens[b]) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
     p = request_span<NR>(a, b);
     const uint32_t n = p.n, C = a.cluster;  // (the product stays below 2^31: at most 8 blocks)
     const int s0 = (rank * n + C - 1) / C;
@@ -287,7 +291,7 @@ __device__ __forceinline__ void run(const Args& a, Tile& tile, unsigned char* st
     if (a.lens) {
       int mine = 0;
       for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-        if (blockIdx.x == 0 && static_cast<uint32_t>(__ldg(a.lens + b)) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
+        if (blockIdx.x == 0 && static_cast<uint32_t>(a.lens[b]) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
         mine += (request_span<NR>(a, b).n + PAD) * a.Hkv;
       }
       int x = mine;

@@ -41,7 +41,7 @@ __device__ __forceinline__ void load_16(uint32_t* w, const void* p, bool live) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
       "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}\n"
+      "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}\n"
       : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3])
       : "l"(p), "r"(static_cast<uint32_t>(live)));
 }
@@ -51,7 +51,7 @@ __device__ __forceinline__ void load_32(uint32_t* w, const void* p, bool live, b
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %9, 0;\n\t"
         "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
         "mov.b32 %4, 0;\n\tmov.b32 %5, 0;\n\tmov.b32 %6, 0;\n\tmov.b32 %7, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t}\n"
+        "@p ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t}\n"
         : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3]), "=&r"(w[4]), "=&r"(w[5]), "=&r"(w[6]), "=&r"(w[7])
         : "l"(p), "r"(static_cast<uint32_t>(live)));
   } else {
@@ -102,7 +102,7 @@ struct RTile {
         a.q + ((static_cast<int64_t>(b) * a.s.nq + i) * a.s.Hq + h * a.s.g + head) * D + i4 * (D / 4));
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) {
-      qs[32 * x] = i < a.s.nq ? __ldg(src + x) : make_uint4(0, 0, 0, 0);  // read by this lane alone
+      qs[32 * x] = i < a.s.nq ? src[x] : make_uint4(0, 0, 0, 0);  // read by this lane alone
     }
   }
 

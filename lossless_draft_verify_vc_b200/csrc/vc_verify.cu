@@ -490,8 +490,18 @@ __global__ void __launch_bounds__(VBlk<RTC>::THREADS) verify_kernel(const __grid
             ps2 = __fadd2_rn(ps2, make_float2(p0, p1));
           else
             psum += p0 + p1;
-          const uint32_t hw = pack_bf2(p0, p1);
-          const float2 lo = __ffma2_rn(unpack_bf2(hw), neg1, make_float2(p0, p1));  // p - bf16(p), exact
+          const float2 pp = make_float2(p0, p1);
+          float2 hi;
+          if constexpr (WIN) {
+            // p to 8 significant bits without unpacking bf16 again (the packed
+            // FMAs share a pipe with nothing else here): t = p (2^16 + 1)
+            // rounded keeps p's first 8 bits above 2^16 p
+            const float2 t = __ffma2_rn(pp, make_float2(65536.f, 65536.f), pp);
+            hi = __ffma2_rn(pp, make_float2(-65536.f, -65536.f), t);
+          }
+          const uint32_t hw = WIN ? pack_bf2(hi.x, hi.y) : pack_bf2(p0, p1);
+          if constexpr (!WIN) hi = unpack_bf2(hw);
+          const float2 lo = __ffma2_rn(hi, neg1, pp);  // p - hi, exact
           phi[c * 16 + j / 2] = hw;
           plo[c * 16 + j / 2] = pack_bf2(lo.x, lo.y);
         }

@@ -59,7 +59,12 @@
 // Up to 8 chunks of a unit run as one thread-block cluster and merge in it:
 // every block leaves its O rows and (m, l) in shared memory, and after a
 // cluster barrier sums its share of the rows from all of them (no partials
-// in memory, no second launch).
+// in memory, no second launch).  Measured on B200 (8 requests x 8 KV heads, 31
+// rows, g = 4, window 4096; 141 MB): 38.9 us of device time against 21.6 at
+// the copy rate.  The tile loop is bound by the softmax warps' instructions
+// (about 13 a score with everything around them; ALU pipe 34%, tensor pipe
+// 33%, issue 39%): key tiles of 128 with one S buffer took 48 us, two
+// warpgroups per row 48.  9 us are start, drain and merge.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -13,9 +13,11 @@
 // products, so a warp always has loads in flight.
 //
 // Bound by HBM for long contexts and by the chain of a block (launch, loads,
-// merge) for short ones.  Measured on B200 against the tcgen05 form:
-// 1 row, g = 4, 8 KV heads, window 1024: ROWS_SHORT; window 8192: ROWS_LONG;
-// 1 x 200K keys, one KV head, g = 8: ROWS_ALL.
+// merge) for short ones.  Measured on B200, us of device time per call, the
+// tcgen05 form against this one: 1 row, g = 4, 8 KV heads, window 1024 10.4 :
+// 7.2, window 8192 16.0 : 13.6, 8 requests with window 4096 33.1 : 27.8; 16
+// requests with window 512 16.5 : 10.0; 2 rows, 2 KV heads, window 4096 10.5 :
+// 10.5; but one KV head of 200K keys 31.2 : 34.0 (148 partials of one unit).
 #include <algorithm>
 
 #include "vc_stream.cuh"

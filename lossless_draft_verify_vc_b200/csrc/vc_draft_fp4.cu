@@ -433,7 +433,7 @@ vc_status check_draft(const vc_attn_shape* sh, const vc_fp4_cache* c, const char
 template <int D, bool HALF>
 void launch_draft(FArgs& a, const stream::Plan& p, uint32_t L, cudaStream_t s) {
   using Tile = FTile<D, HALF>;
-  static stream::Launcher<FArgs> k{draft_fp4_kernel<D, HALF>, Tile::SMEM_B};
+  static stream::Launcher<FArgs> k(draft_fp4_kernel<D, HALF>, Tile::SMEM_B);
   const int n = stream::choose(a.s, p, L, Tile::NR, Tile::PAD, Tile::MIN, Tile::GAIN, [&](int C) { return k.active(C); });
   k.launch(a, n, a.s.cluster, s);
 }

@@ -65,10 +65,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return unpack_bf2(w);
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.u16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+// max(|a|, |b|) of both halves, NaN if one is NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+  const T2 m = __hmax2_nan(__habs2(*reinterpret_cast<T2*>(&a)), __habs2(*reinterpret_cast<T2*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
 // Values of NW words and their largest |x| * down.  Patterns of |x| are
@@ -76,9 +78,9 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 // instead) or values past the scales' range (clamped to it) is flagged.
 template <typename T, int NW>
 __device__ __forceinline__ float take(const uint32_t* w, float (&x)[2 * NW], float down, bool& odd) {
-  uint32_t m = w[0] & 0x7fff7fffu;
+  uint32_t m = w[0];
 #pragma unroll
-  for (int i = 1; i < NW; ++i) m = max_u16x2(m, w[i] & 0x7fff7fffu);
+  for (int i = 1; i < NW; ++i) m = max_abs2<T>(m, w[i]);
   m = max(m & 0xffffu, m >> 16);
 #pragma unroll
   for (int i = 0; i < NW; ++i) {

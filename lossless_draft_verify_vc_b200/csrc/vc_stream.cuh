@@ -28,6 +28,8 @@
 // block of 4 warps more per SM cost 5 us of 66 at 8 x 32K tokens).
 #pragma once
 
+#include <atomic>
+
 #include "vc_splitk.cuh"
 
 namespace vc {
@@ -529,10 +531,11 @@ template <class Params>
 struct Launcher {
   void (*kernel)(Params);
   int smem;
+  Launcher(void (*k)(Params), int bytes) : kernel(k), smem(bytes) {}
   struct Device {
-    bool set;
-    int active[4];  // clusters of 1, 2, 4, 8 blocks that the device holds, + 1
-  } dev[64] = {};
+    std::atomic<bool> set{false};
+    int active[4];  // clusters of 1, 2, 4, 8 blocks that the device holds
+  } dev[64];
 
   void fill(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int n, int cluster, cudaStream_t s) const {
     cfg.gridDim = dim3(static_cast<unsigned>(n));
@@ -550,7 +553,7 @@ struct Launcher {
   Device& device() {
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) d = 0;
-    if (!dev[d].set) {
+    if (!dev[d].set.load(std::memory_order_acquire)) {
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       for (int i = 0, C = 1; i < 4; ++i, C *= 2) {
         cudaLaunchConfig_t cfg = {};
@@ -565,7 +568,7 @@ struct Launcher {
         }
         dev[d].active[i] = n;
       }
-      dev[d].set = true;
+      dev[d].set.store(true, std::memory_order_release);
     }
     return dev[d];
   }

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(stream::kThreads, 1) verify_rows_kernel(RArgs 
 template <int D>
 void launch_rows(RArgs& a, const stream::Plan& p, cudaStream_t s) {
   using Tile = RTile<D>;
-  static stream::Launcher<RArgs> k{verify_rows_kernel<D>, Tile::SMEM_B};
+  static stream::Launcher<RArgs> k(verify_rows_kernel<D>, Tile::SMEM_B);
   const int n = stream::choose(a.s, p, static_cast<uint32_t>(a.T), Tile::NR, Tile::PAD, Tile::MIN, Tile::GAIN,
                                [&](int C) { return k.active(C); });
   k.launch(a, n, a.s.cluster, s);

@@ -256,7 +256,7 @@ __device__ __forceinline__ float warp_max_xor(float v, int lanemask) {
 // A head's power of two (clamped so that it and its inverse are normal).
 __device__ __forceinline__ float two_to(const int32_t* exp, int h, int sign) {
   if (!exp) return 1.f;
-  const int e = min(60, max(-60, exp[h])) * sign;
+  const int e = min(60, max(-60, __ldcg(exp + h))) * sign;
   return __int_as_float((e + 127) << 23);
 }
 

@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(stream::kThreads, 1) draft_fp4_kernel(FArgs a)
   using Tile = FTile<D, HALF>;
   extern __shared__ __align__(128) unsigned char smem[];
   Tile tile(a, smem);
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   stream::run(a.s, tile, smem + Tile::STATE_OFF, smem);
 }
 

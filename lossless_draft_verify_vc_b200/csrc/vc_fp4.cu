@@ -138,14 +138,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_write_kernel(
   constexpr int VW = D / 16;  // words of a lane's V run (16 or 8 channels)
   const int unit = blockIdx.y, lane = threadIdx.x & 31;
   const int b = unit / Hkv, h = unit - b * Hkv;
-  // the next call's blocks may be scheduled as this grid's retire; they wait
-  // here for its end, as these do for the call before
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // (in this order: the next call's blocks may be scheduled as this grid's
+  // retire, but not while the grid before it still writes)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const float kdown = two_to(k_exp, h, -1), vdown = two_to(v_exp, h, -1);
   int64_t p, c;
   if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
   const bool kwide = aligned32(k), vwide = aligned32(v);
-  const float kdown = two_to(k_exp, h, -1), vdown = two_to(v_exp, h, -1);
   const int64_t last = (p + c - 1) / kHalfTok;
   const int kt = lane >> 2, vt = 2 * (lane & 3);
   bool odd = false;
@@ -278,14 +278,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) fp4_read_kernel(
   constexpr int VN = D / 8;  // channels of a lane's V run
   const int unit = blockIdx.y, lane = threadIdx.x & 31;
   const int b = unit / Hkv, h = unit - b * Hkv;
-  // the next call's blocks may be scheduled as this grid's retire; they wait
-  // here for its end, as these do for the call before
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // (in this order: the next call's blocks may be scheduled as this grid's
+  // retire, but not while the grid before it still writes)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const float kup = two_to(k_exp, h, 1), vup = two_to(v_exp, h, 1);
   int64_t p, c;
   if (!fp4_span(pos, pos0, counts, b, n, T_cap, flags, threadIdx.x == 0, p, c) || c == 0) return;
   const bool kwide = aligned32(k), vwide = aligned32(v);
-  const float kup = two_to(k_exp, h, 1), vup = two_to(v_exp, h, 1);
   const int64_t last = (p + c - 1) / kHalfTok;
   const int kt = lane >> 2, vt = 2 * (lane & 3);
 #pragma unroll 1

@@ -21,7 +21,9 @@
 //
 // Both kernels are programmatic dependents, resident while the call before
 // them still writes: nothing is read before griddepcontrol.wait, and nothing
-// through the read-only path.
+// through the read-only path.  The wait comes before launch_dependents, so a
+// grid that is scheduled early finds only its direct predecessor unfinished,
+// which is what a caller promises about with VC_CACHE_STATIC.
 //
 // Code outside the stage loop is kept short rather than fast: it runs once or
 // twice per block out of an empty instruction cache (unrolled merges and one

@@ -244,8 +244,8 @@ template <int D>
 __global__ void __launch_bounds__(stream::kThreads, 1) verify_rows_kernel(RArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   RTile<D> tile(a, smem);
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   stream::run(a.s, tile, smem, smem);
 }
 

@@ -208,16 +208,17 @@ def _arg(name: str, x, dtypes, n: int, optional: bool = False, dev: int | None =
     the current device (dev, when the caller has looked it up), of one of
     `dtypes` and of at least n elements.  Integers (raw device pointers) pass
     through."""
+    if x is None and optional:
+        return 0
     try:
-        if x.dtype in dtypes and x.numel() >= n and x.is_contiguous() and 0 <= x.get_device() == (_device() if dev is None else dev):
+        if x.dtype in dtypes and x.numel() >= n and x.is_contiguous() and 0 <= x.get_device() == (
+                _device() if dev is None else dev):
             return x.data_ptr()
     except AttributeError:
         if isinstance(x, int):
             return x
         if x is not None:
             raise
-        if optional:
-            return 0
         raise ValueError(f"{name} is missing") from None
     if x.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)} (got {x.dtype})")
@@ -231,12 +232,15 @@ def _arg(name: str, x, dtypes, n: int, optional: bool = False, dev: int | None =
 def _current(x) -> int:
     """The current device if the tensor x is on it, else -1 (which no tensor passes)."""
     if isinstance(x, int):
-        return _device()
+        return _device() if torch.cuda.is_initialized() else -1
     return x.get_device() if x is not None and 0 <= x.get_device() == _device() else -1
 
 
-def _stream(stream) -> int:
+def _stream(stream, dev: int = -1) -> int:
+    """Handle of a stream; default: the current one (of device dev, when the caller has looked it up)."""
     if stream is None:
+        if dev >= 0:
+            return _raw_stream(dev)
         return _raw_stream(_device()) if torch.cuda.is_initialized() else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -349,12 +353,14 @@ def vc_verify_attn_window(sh, q, k, v, T: int, nq: int, out, lse, ws, window: in
         ctypes.byref(sh), _arg("q", q, _BF16, no * D, False, dev), _arg("k", k, _BF16, nk, False, dev),
         _arg("v", v, _BF16, nk, False, dev), int(T), _arg("lens", lens, _I32, B, True, dev), int(nq), int(window),
         int(n_sink), _arg("out", out, _F32, no * D, False, dev), _arg("lse", lse, _F32, no, True, dev),
-        _arg("ws", ws, _U8, 0, False, dev), _size(ws), _stream(stream)))
+        _arg("ws", ws, _U8, 0, False, dev), _size(ws), _stream(stream, dev)))
 
 
-def _fp4_match(sh, fc):
-    if getattr(fc, "_dims", None) not in (None, (sh.B, sh.Hkv, sh.D)):  # (a descriptor from fp4_cache)
-        raise ValueError(f"the cache holds (B, Hkv, D) = {fc._dims}, the shape says {(sh.B, sh.Hkv, sh.D)}")
+def _fp4_dims(sh, fc):
+    dims = sh.B, sh.Hkv, sh.D
+    if getattr(fc, "_dims", dims) != dims:  # (a descriptor from fp4_cache)
+        raise ValueError(f"the cache holds (B, Hkv, D) = {fc._dims}, the shape says {dims}")
+    return dims
 
 
 def _size(ws) -> int:
@@ -362,22 +368,22 @@ def _size(ws) -> int:
 
 
 def _fp4_rows(f, sh, fc, k, v, dtypes, n, ws, pos, pos0, counts, dtype, stream):
-    _fp4_match(sh, fc)
+    B, Hkv, D = _fp4_dims(sh, fc)
+    kt, vt = getattr(k, "dtype", None), getattr(v, "dtype", None)
     if dtype is None:
-        if isinstance(k, int) or isinstance(v, int):
+        if kt is None or vt is None:
             raise ValueError("raw pointers need dtype")
-        dtype = k.dtype
-    if not isinstance(k, int) and not isinstance(v, int) and k.dtype != v.dtype:
+        dtype = kt
+    if kt is not vt and kt is not None and vt is not None:
         raise ValueError("k and v must have the same dtype")
     if dtype not in dtypes:
         raise ValueError(f"k and v must be {' or '.join(str(d) for d in dtypes)} (got {dtype})")
-    dtypes = (dtype,)
-    B, dev = sh.B, _current(k)
-    size = B * sh.Hkv * int(n) * sh.D
+    n, dev, dtypes = int(n), _current(k), (dtype,)
+    size = B * Hkv * n * D
     _check(f(ctypes.byref(sh), ctypes.byref(fc), _arg("k", k, dtypes, size, False, dev),
-             _arg("v", v, dtypes, size, False, dev), _CODES[dtype], int(n), _arg("pos", pos, _I32, B, True, dev),
+             _arg("v", v, dtypes, size, False, dev), _CODES[dtype], n, _arg("pos", pos, _I32, B, True, dev),
              int(pos0), _arg("counts", counts, _I32, B, True, dev), _arg("ws", ws, _U8, 0, False, dev), _size(ws),
-             _stream(stream)))
+             _stream(stream, dev)))
 
 
 def vc_fp4_cache_write(sh, fc, k, v, n: int, ws, pos=None, pos0: int = 0, counts=None, dtype=None, stream=None):
@@ -403,13 +409,13 @@ def vc_draft_attn_fp4_workspace_size(sh, fc) -> int:
 def vc_draft_attn_fp4(sh, fc, q, out, ws, lse=None, window: int = 0, n_sink: int = 0, stream=None):
     """Draft attention over a 4-bit floating-point cache, optionally limited
     to a sliding window and the first n_sink tokens (see include/vc.h)."""
-    _fp4_match(sh, fc)
-    n, dev = sh.B * sh.Hq, _current(q)
-    size = n * sh.D
+    B, _, D = _fp4_dims(sh, fc)
+    n, dev = B * sh.Hq, _current(q)
+    size = n * D
     _check(lib().vc_draft_attn_fp4(ctypes.byref(sh), ctypes.byref(fc), int(window), int(n_sink),
                                    _arg("q", q, _BF16, size, False, dev), _arg("out", out, _F32, size, False, dev),
                                    _arg("lse", lse, _F32, n, True, dev), _arg("ws", ws, _U8, 0, False, dev), _size(ws),
-                                   _stream(stream)))
+                                   _stream(stream, dev)))
 
 
 def vc_accept_workspace_size(B: int, K: int, V: int) -> int:

@@ -61,10 +61,14 @@
 // cluster barrier sums its share of the rows from all of them (no partials
 // in memory, no second launch).  Measured on B200 (8 requests x 8 KV heads, 31
 // rows, g = 4, window 4096; 141 MB): 38.9 us of device time against 21.6 at
-// the copy rate.  The tile loop is bound by the softmax warps' instructions
-// (about 13 a score with everything around them; ALU pipe 34%, tensor pipe
-// 33%, issue 39%): key tiles of 128 with one S buffer took 48 us, two
-// warpgroups per row 48.  9 us are start, drain and merge.
+// the copy rate: 9 us of start, drain and merge, and a tile loop at 4.7 TB/s
+// that waits on its own round trips (load, S, softmax, P.V) rather than on one
+// unit: ALU pipe 34%, tensor pipe 33%, issue 39%.  Without any softmax work it
+// took 34.6 us (g = 5, window 16000: 52.3 of 54.2), without the low parts'
+// product 38.1 (53.1), without both 31.2 (43.9).  Key tiles of 128 with one S
+// buffer took 48 us, two warpgroups per row 48, two warpgroups taking turns at
+// the tiles 43.5 (61.9), the same with one block per SM, 4 S buffers and 5
+// stages 50 (85).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -296,7 +296,7 @@ VC_API vc_status vc_compact_kept(const vc_attn_shape* shape, const void* k, cons
  *   x_hat = e2m1 value * s * 2^exp[h]
  *
  * both roundings to nearest, ties to the even code, decided as an exact
- * division decides; a negative x that rounds to zero keeps its sign.  exp is
+ * division decides; a zero, and an x that rounds to zero, keeps its sign.  exp is
  * an optional power of two per KV head that moves the head's values into the
  * scales' range (about 0.02 .. 2688 as a block's largest value).  Every token
  * is quantised by itself -- no group of tokens has to fill up first, unlike

@@ -73,22 +73,25 @@ __device__ __forceinline__ uint32_t floats_to_codes(const float* x) {
 }
 
 // Quotients of numbers with few significant bits, as the roundings below need
-// them: x * (hi + lo) with hi + lo = 1 / d up to 2^-45 of itself is off by so
+// them: x * (hi + lo) with hi + lo = 1 / d up to 2^-42 of itself is off by so
 // little that one fp32 rounding returns x / d itself where that is a number
 // of at most 20 significant bits, such as the border between two codes (e2m1:
 // 3 bits, e4m3: 5).  Any other x / d differs from a border by at least 2^-11
 // of it (x has at most 11 bits -- bf16, fp16 -- and border * d at most 8), so
-// every rounding decides as exact division does.
+// every rounding decides as exact division does.  hi is below 1 / d, so that
+// lo >= 0 and a zero keeps its sign (x = -0: -0 + -0; with lo < 0 it would be
+// -0 + +0 = +0).
 struct Recip {
   float hi, lo;
   __device__ __forceinline__ float2 times(float2 x) const {  // two numbers per instruction
     return __ffma2_rn(x, make_float2(hi, hi), __fmul2_rn(x, make_float2(lo, lo)));
   }
 };
-__device__ __forceinline__ Recip recip(float d) {  // 1 / d; 0 for d = 0
+__device__ __forceinline__ Recip recip(float d) {  // 1 / d for d > 0
   Recip r;
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r.hi) : "f"(d));
-  r.hi = d > 0.f ? r.hi : 0.f;
+  // (off by at most one step; two steps down it is 1 to 3 below)
+  r.hi = __int_as_float(__float_as_int(r.hi) - 2);
   r.lo = fmaf(-d, r.hi, 1.f) * r.hi;
   return r;
 }
@@ -105,7 +108,7 @@ __device__ __forceinline__ uint8_t block_scale(float amax) {
 template <int N>
 __device__ __forceinline__ void quantise_codes(float (&x)[N], uint8_t s8, float down, uint32_t (&codes)[N / 8]) {
   const float s = scale_to_float(s8);
-  Recip r = recip(s);
+  Recip r = recip(s);  // (s = 0: not used)
   r.hi *= down, r.lo *= down;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {

@@ -122,6 +122,7 @@ struct FTile {
       fence_mbar_init();
       fence_proxy_async_smem();
     }
+    __syncwarp();  // the other lanes wait on them
   }
 
   // bf16 query words of this lane: its tile column's head, D / 4 channels from

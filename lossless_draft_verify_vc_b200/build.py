@@ -34,7 +34,8 @@ def _nvcc() -> str:
 
 
 def _headers():
-    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    return [h for d, e in ((CSRC, "*.cuh"), (CSRC, "*.h"), (os.path.join(ROOT, "include"), "*.h"))
+            for h in glob.glob(os.path.join(d, e))]
 
 
 def _stale(src: str, obj: str, hdr_mtime: float) -> bool:

@@ -30,8 +30,7 @@
 // block of 4 warps more per SM cost 5 us of 66 at 8 x 32K tokens).
 #pragma once
 
-#include <atomic>
-
+#include "vc_once.h"
 #include "vc_splitk.cuh"
 
 namespace vc {
@@ -535,9 +534,9 @@ struct Launcher {
   int smem;
   Launcher(void (*k)(Params), int bytes) : kernel(k), smem(bytes) {}
   struct Device {
-    std::atomic<bool> set{false};
     int active[4];  // clusters of 1, 2, 4, 8 blocks that the device holds
-  } dev[64];
+  };
+  PerDevice<Device> devices;
 
   void fill(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, int n, int cluster, cudaStream_t s) const {
     cfg.gridDim = dim3(static_cast<unsigned>(n));
@@ -552,10 +551,10 @@ struct Launcher {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
   }
-  Device& device() {
+  const Device& device() {
     int d = 0;
-    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= 64) d = 0;
-    if (!dev[d].set.load(std::memory_order_acquire)) {
+    if (cudaGetDevice(&d) != cudaSuccess) d = 0;
+    return devices.get(d, [&](Device& dev) {
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       for (int i = 0, C = 1; i < 4; ++i, C *= 2) {
         cudaLaunchConfig_t cfg = {};
@@ -568,11 +567,9 @@ struct Launcher {
           cudaGetLastError();
           n = 0;
         }
-        dev[d].active[i] = n;
+        dev.active[i] = n;
       }
-      dev[d].set.store(true, std::memory_order_release);
-    }
-    return dev[d];
+    });
   }
   int active(int C) { return device().active[C == 8 ? 3 : C == 4 ? 2 : C == 2 ? 1 : 0]; }
   void launch(const Params& a, int n, int cluster, cudaStream_t s) {

@@ -76,6 +76,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "vc_once.h"
 #include "vc_splitk.cuh"
 #include "vc_tc.cuh"
 #include "vc_verify_rows.h"
@@ -870,21 +871,17 @@ struct VPlan {
 template <int D, int RTC, bool WIN>
 int verify_occupancy() {
   using C = VCfg<D, RTC>;
-  static int cache[64] = {0};
+  static PerDevice<int> blocks;
   int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) dev = 0;
-  if (cache[dev] == 0) {
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  return blocks.get(dev, [](int& n) {
     const int smem = WIN ? C::SMEM_WIN_B : C::SMEM_B;
     cudaFuncSetAttribute(verify_kernel<D, RTC, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, verify_kernel<D, RTC, WIN>, VBlk<RTC>::THREADS, smem) !=
             cudaSuccess ||
         n < 1)
       n = 1;
-    cache[dev] = n;
-  }
-  return cache[dev];
+  });
 }
 
 // Split of the context into C chunks per unit: the C that

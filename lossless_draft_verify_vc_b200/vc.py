@@ -290,6 +290,7 @@ def fp4_cache(records, T=None, lens=None, k_exp=None, v_exp=None) -> vc_fp4_cach
                      _arg("v_exp", v_exp, _I32, Hkv, True))
     d._keep = (records, lens, k_exp, v_exp)
     d._dims = (B, Hkv, records.shape[3] // 18)
+    d._dev = records.get_device()
     return d
 
 
@@ -356,10 +357,14 @@ def vc_verify_attn_window(sh, q, k, v, T: int, nq: int, out, lse, ws, window: in
         _arg("ws", ws, _U8, 0, False, dev), _size(ws), _stream(stream, dev)))
 
 
-def _fp4_dims(sh, fc):
+def _fp4_dims(sh, fc, dev):
+    """(B, Hkv, D) after checking a descriptor from fp4_cache against the shape
+    and the current device (dev; -1: a tensor that is refused anyway)."""
     dims = sh.B, sh.Hkv, sh.D
-    if getattr(fc, "_dims", dims) != dims:  # (a descriptor from fp4_cache)
+    if getattr(fc, "_dims", dims) != dims:
         raise ValueError(f"the cache holds (B, Hkv, D) = {fc._dims}, the shape says {dims}")
+    if getattr(fc, "_dev", dev) != dev >= 0:
+        raise ValueError(f"the cache is on CUDA device {fc._dev}, the current device is {dev}")
     return dims
 
 
@@ -368,7 +373,8 @@ def _size(ws) -> int:
 
 
 def _fp4_rows(f, sh, fc, k, v, dtypes, n, ws, pos, pos0, counts, dtype, stream):
-    B, Hkv, D = _fp4_dims(sh, fc)
+    dev = _current(k)
+    B, Hkv, D = _fp4_dims(sh, fc, dev)
     kt, vt = getattr(k, "dtype", None), getattr(v, "dtype", None)
     if dtype is None:
         if kt is None or vt is None:
@@ -378,7 +384,7 @@ def _fp4_rows(f, sh, fc, k, v, dtypes, n, ws, pos, pos0, counts, dtype, stream):
         raise ValueError("k and v must have the same dtype")
     if dtype not in dtypes:
         raise ValueError(f"k and v must be {' or '.join(str(d) for d in dtypes)} (got {dtype})")
-    n, dev, dtypes = int(n), _current(k), (dtype,)
+    n, dtypes = int(n), (dtype,)
     size = B * Hkv * n * D
     _check(f(ctypes.byref(sh), ctypes.byref(fc), _arg("k", k, dtypes, size, False, dev),
              _arg("v", v, dtypes, size, False, dev), _CODES[dtype], n, _arg("pos", pos, _I32, B, True, dev),
@@ -409,8 +415,9 @@ def vc_draft_attn_fp4_workspace_size(sh, fc) -> int:
 def vc_draft_attn_fp4(sh, fc, q, out, ws, lse=None, window: int = 0, n_sink: int = 0, stream=None):
     """Draft attention over a 4-bit floating-point cache, optionally limited
     to a sliding window and the first n_sink tokens (see include/vc.h)."""
-    B, _, D = _fp4_dims(sh, fc)
-    n, dev = B * sh.Hq, _current(q)
+    dev = _current(q)
+    B, _, D = _fp4_dims(sh, fc, dev)
+    n = B * sh.Hq
     size = n * D
     _check(lib().vc_draft_attn_fp4(ctypes.byref(sh), ctypes.byref(fc), int(window), int(n_sink),
                                    _arg("q", q, _BF16, size, False, dev), _arg("out", out, _F32, size, False, dev),

@@ -688,6 +688,22 @@ VC_API vc_status vc_debug_verify_abort(const vc_attn_shape* shape, const void* q
                                        int64_t T, int nq, float* out, float* lse, void* ws, size_t ws_bytes,
                                        int skip_tile, int64_t limit_ns, void* stream);
 
+/* vc_debug_verify_window_abort does the same to vc_verify_attn_window (more
+ * than 8 rows per KV head): a block that has tile skip_tile of its chunk stops,
+ * and its chunk counts as without keys where the chunks meet in a cluster.
+ * vc_debug_draft_fp4_abort is vc_draft_attn_fp4 with warp stuck_warp (0 .. 15)
+ * of every block waiting for its first copies longer than limit_ns: they are
+ * made, but their barrier expects one arrival more.  The warp gives up, waits
+ * for its copies in flight and adds nothing to its rows.  Both raise
+ * VC_FLAG_WAIT_TIMEOUT; the rows concerned are not valid. */
+VC_API vc_status vc_debug_verify_window_abort(const vc_attn_shape* shape, const void* q, const void* k, const void* v,
+                                              int64_t T, const int32_t* lens, int nq, int64_t window, int64_t n_sink,
+                                              float* out, float* lse, void* ws, size_t ws_bytes, int skip_tile,
+                                              int64_t limit_ns, void* stream);
+VC_API vc_status vc_debug_draft_fp4_abort(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window,
+                                          int64_t n_sink, const void* q, float* out, float* lse, void* ws,
+                                          size_t ws_bytes, int stuck_warp, int64_t limit_ns, void* stream);
+
 /* vc_debug_quant_partition reports, without touching a GPU, how
  * vc_draft_attn_quant cuts one call into blocks when at most target_blocks
  * blocks are allowed (the real call uses SMs x resident blocks).  Each

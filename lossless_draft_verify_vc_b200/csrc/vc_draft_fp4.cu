@@ -50,6 +50,11 @@ struct FArgs {
   const __nv_bfloat16* q;
   const int32_t* k_exp;
   float scale_log2;
+  // failure-path test only (vc_debug_draft_fp4_abort): the warp of every block
+  // whose first stage never counts as landed (-1: none), and the limit of the
+  // stages' waits
+  int stuck_warp;
+  uint64_t wait_ns;
 };
 
 // mma_f16 into zeros
@@ -118,7 +123,7 @@ struct FTile {
     ring = smem + warp * RING;
     bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF) + warp * NST;
     if (lane == 0) {
-      for (int i = 0; i < NST; ++i) mbar_init(&bars[i], 1);
+      for (int i = 0; i < NST; ++i) mbar_init(&bars[i], i == 0 && warp == a.stuck_warp ? 2 : 1);
       fence_mbar_init();
       fence_proxy_async_smem();
     }
@@ -215,7 +220,7 @@ struct FTile {
   __device__ __forceinline__ bool stage(const Span& p, int x, int) {
     const bool full = x >= p.f0 && x < p.f1;
     if (!__all_sync(0xffffffffu, mbar_try_wait_hint(&bars[slot], phase, 20000u)) &&
-        __any_sync(0xffffffffu, !mbar_wait_bounded(&bars[slot], phase, a.s.flags)))
+        __any_sync(0xffffffffu, !mbar_wait_bounded(&bars[slot], phase, a.s.flags, a.wait_ns)))
       return false;
     const unsigned char* st = ring + slot * STAGE;
     if (++slot == NST) slot = 0, phase ^= 1;
@@ -439,33 +444,26 @@ void launch_draft(FArgs& a, const stream::Plan& p, uint32_t L, cudaStream_t s) {
   k.launch(a, n, a.s.cluster, s);
 }
 
-}  // namespace
-}  // namespace vc
-
-extern "C" {
-
-size_t vc_draft_attn_fp4_workspace_size(const vc_attn_shape* shape, const vc_fp4_cache* cache) {
-  if (vc::check_draft(shape, cache, "vc_draft_attn_fp4_workspace_size") != VC_OK) return 0;
-  return vc::stream::plan(shape->Hq / shape->Hkv, shape->D).total;
-}
-
-vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window, int64_t n_sink,
-                            const void* q, float* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
-  vc_status st = vc::check_draft(shape, cache, "vc_draft_attn_fp4");
+vc_status draft_call(const char* who, const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window,
+                     int64_t n_sink, const void* q, float* out, float* lse, void* ws, size_t ws_bytes, int stuck_warp,
+                     uint64_t wait_ns, void* stream_) {
+  vc_status st = check_draft(shape, cache, who);
   if (st != VC_OK) return st;
-  VC_REQUIRE(window >= 0 && n_sink >= 0, "vc_draft_attn_fp4: window and n_sink must be >= 0");
-  VC_REQUIRE(cache->records && q && out && ws, "vc_draft_attn_fp4: null pointer argument");
-  VC_REQUIRE(vc::aligned16(cache->records) && vc::aligned16(q) && vc::aligned16(out) && vc::aligned16(ws),
-             "vc_draft_attn_fp4: records, q, out and workspace must be 16-byte aligned");
+  VC_REQUIRE(window >= 0 && n_sink >= 0, "%s: window and n_sink must be >= 0", who);
+  VC_REQUIRE(cache->records && q && out && ws, "%s: null pointer argument", who);
+  VC_REQUIRE(aligned16(cache->records) && aligned16(q) && aligned16(out) && aligned16(ws),
+             "%s: records, q, out and workspace must be 16-byte aligned", who);
   const int g = shape->Hq / shape->Hkv;
-  const vc::stream::Plan p = vc::stream::plan(g, shape->D);
-  VC_REQUIRE(ws_bytes >= p.total, "vc_draft_attn_fp4: workspace too small (%zu < %zu)", ws_bytes, p.total);
-  vc::FArgs a{};
+  const stream::Plan p = stream::plan(g, shape->D);
+  VC_REQUIRE(ws_bytes >= p.total, "%s: workspace too small (%zu < %zu)", who, ws_bytes, p.total);
+  FArgs a{};
   a.records = static_cast<const uint8_t*>(cache->records);
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k_exp = cache->k_exp;
   const float sm = shape->sm_scale > 0.f ? shape->sm_scale : 1.0f / sqrtf(static_cast<float>(shape->D));
   a.scale_log2 = sm * 1.4426950408889634f;
+  a.stuck_warp = stuck_warp;
+  a.wait_ns = wait_ns;
   a.s.out = out;
   a.s.lse = lse;
   a.s.lens = cache->lens;
@@ -480,14 +478,41 @@ vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cach
   a.s.Hkv = shape->Hkv;
   a.s.g = g;
   a.s.nq = 1;
-  vc::stream::bind_workspace(a.s, p, ws);
+  stream::bind_workspace(a.s, p, ws);
   const uint32_t L = static_cast<uint32_t>(cache->lens ? cache->T_cap : cache->T);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaStream_t s = static_cast<cudaStream_t>(stream_);
   if (shape->D == 128)
-    g <= 4 ? vc::launch_draft<128, true>(a, p, L, s) : vc::launch_draft<128, false>(a, p, L, s);
+    g <= 4 ? launch_draft<128, true>(a, p, L, s) : launch_draft<128, false>(a, p, L, s);
   else
-    g <= 4 ? vc::launch_draft<64, true>(a, p, L, s) : vc::launch_draft<64, false>(a, p, L, s);
-  return vc::launch_status("vc_draft_attn_fp4");
+    g <= 4 ? launch_draft<64, true>(a, p, L, s) : launch_draft<64, false>(a, p, L, s);
+  return launch_status(who);
+}
+
+}  // namespace
+}  // namespace vc
+
+extern "C" {
+
+size_t vc_draft_attn_fp4_workspace_size(const vc_attn_shape* shape, const vc_fp4_cache* cache) {
+  if (vc::check_draft(shape, cache, "vc_draft_attn_fp4_workspace_size") != VC_OK) return 0;
+  return vc::stream::plan(shape->Hq / shape->Hkv, shape->D).total;
+}
+
+vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window, int64_t n_sink,
+                            const void* q, float* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  return vc::draft_call("vc_draft_attn_fp4", shape, cache, window, n_sink, q, out, lse, ws, ws_bytes, -1, 2000000000ull,
+                        stream);
+}
+
+vc_status vc_debug_draft_fp4_abort(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window,
+                                   int64_t n_sink, const void* q, float* out, float* lse, void* ws, size_t ws_bytes,
+                                   int stuck_warp, int64_t limit_ns, void* stream) {
+  VC_REQUIRE(stuck_warp >= 0 && stuck_warp < vc::stream::kWarps,
+             "vc_debug_draft_fp4_abort: stuck_warp must be 0 .. 15 (got %d)", stuck_warp);
+  VC_REQUIRE(limit_ns >= 1000 && limit_ns <= 100000000,
+             "vc_debug_draft_fp4_abort: limit must be 1 us .. 100 ms (got %lld ns)", static_cast<long long>(limit_ns));
+  return vc::draft_call("vc_debug_draft_fp4_abort", shape, cache, window, n_sink, q, out, lse, ws, ws_bytes, stuck_warp,
+                        static_cast<uint64_t>(limit_ns), stream);
 }
 
 }  // extern "C"

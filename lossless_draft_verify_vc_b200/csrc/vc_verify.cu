@@ -1093,6 +1093,16 @@ vc_status verify_launch(const vc_attn_shape* shape, const void* q, const void* k
   }
   return vc::launch_status(who);
 }
+vc_status verify_window(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T,
+                        const int32_t* lens, int nq, int64_t window, int64_t n_sink, float* out, float* lse, void* ws,
+                        size_t ws_bytes, void* stream, int skip_k, uint64_t wait_ns) {
+  VC_REQUIRE(window >= 0 && n_sink >= 0, "vc_verify_attn_window: window and n_sink must be >= 0");
+  // no position reaches 2^31: larger values mean the same and would overflow
+  window = window >= T ? 0 : window;
+  n_sink = std::min<int64_t>(n_sink, INT32_MAX);
+  return verify_launch<true>(shape, q, k, v, T, lens, nq, window, n_sink, out, lse, ws, ws_bytes, stream, skip_k,
+                             wait_ns);
+}
 }  // namespace
 }  // namespace vc
 
@@ -1119,12 +1129,23 @@ size_t vc_verify_attn_window_workspace_size(const vc_attn_shape* shape, int64_t 
 vc_status vc_verify_attn_window(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T,
                                 const int32_t* lens, int nq, int64_t window, int64_t n_sink, float* out, float* lse,
                                 void* ws, size_t ws_bytes, void* stream) {
-  VC_REQUIRE(window >= 0 && n_sink >= 0, "vc_verify_attn_window: window and n_sink must be >= 0");
-  // no position reaches 2^31: larger values mean the same and would overflow
-  window = window >= T ? 0 : window;
-  n_sink = std::min<int64_t>(n_sink, INT32_MAX);
-  return vc::verify_launch<true>(shape, q, k, v, T, lens, nq, window, n_sink, out, lse, ws, ws_bytes, stream, -1,
-                                 2000000000ull);
+  return vc::verify_window(shape, q, k, v, T, lens, nq, window, n_sink, out, lse, ws, ws_bytes, stream, -1,
+                           2000000000ull);
+}
+
+vc_status vc_debug_verify_window_abort(const vc_attn_shape* shape, const void* q, const void* k, const void* v,
+                                       int64_t T, const int32_t* lens, int nq, int64_t window, int64_t n_sink,
+                                       float* out, float* lse, void* ws, size_t ws_bytes, int skip_tile,
+                                       int64_t limit_ns, void* stream) {
+  const char* who = "vc_debug_verify_window_abort";
+  VC_REQUIRE(skip_tile >= 0, "%s: skip_tile must be >= 0 (got %d)", who, skip_tile);
+  VC_REQUIRE(limit_ns >= 1000 && limit_ns <= 100000000, "%s: limit must be 1 us .. 100 ms (got %lld ns)", who,
+             static_cast<long long>(limit_ns));
+  vc_status st = vc::check_verify(shape, T, 1, who);
+  if (st != VC_OK) return st;
+  VC_REQUIRE(!vc::verify_rows_apply(*shape, nq), "%s: calls of at most 8 rows per KV head wait for nothing", who);
+  return vc::verify_window(shape, q, k, v, T, lens, nq, window, n_sink, out, lse, ws, ws_bytes, stream, skip_tile,
+                           static_cast<uint64_t>(limit_ns));
 }
 
 vc_status vc_debug_verify_abort(const vc_attn_shape* shape, const void* q, const void* k, const void* v, int64_t T,

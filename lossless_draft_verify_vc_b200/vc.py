@@ -142,6 +142,11 @@ def lib() -> ctypes.CDLL:
                                           c_void_p]),
             "vc_compact_kept": (c_int, [P(vc_attn_shape), c_void_p, c_void_p, ctypes.c_int64, c_void_p, c_int,
                                         c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+            "vc_debug_verify_window_abort": (c_int, [P(vc_attn_shape), c_void_p, c_void_p, c_void_p, c_int64, c_void_p,
+                                                     c_int, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_size_t,
+                                                     c_int, c_int64, c_void_p]),
+            "vc_debug_draft_fp4_abort": (c_int, [P(vc_attn_shape), P(vc_fp4_cache), c_int64, c_int64, c_void_p,
+                                                 c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_int64, c_void_p]),
             "vc_debug_quant_partition": (c_int, [P(vc_attn_shape), P(vc_quant_cache), c_int, c_void_p, c_int,
                                                  P(c_int), P(c_int), P(c_int), P(c_int), P(c_int)]),
             "vc_kvstream_create": (c_int, [P(c_void_p), c_int, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p,
@@ -494,6 +499,24 @@ def vc_debug_verify_abort(sh, q, k, v, T: int, nq: int, out, lse, ws, skip_tile:
     _check(lib().vc_debug_verify_abort(ctypes.byref(sh), _p(q), _p(k), _p(v), int(T), int(nq), _p(out), _p(lse),
                                        _p(ws), ws.numel() if hasattr(ws, "numel") else 1 << 62, int(skip_tile),
                                        int(limit_ns), _stream(stream)))
+
+
+def vc_debug_verify_window_abort(sh, q, k, v, T: int, nq: int, out, lse, ws, skip_tile: int, limit_ns: int,
+                                 window: int = 0, n_sink: int = 0, lens=None, stream=None):
+    """vc_verify_attn_window with K tile skip_tile of every block never
+    requested and the waits giving up after limit_ns (see include/vc.h)."""
+    _check(lib().vc_debug_verify_window_abort(ctypes.byref(sh), _p(q), _p(k), _p(v), int(T), _p(lens), int(nq),
+                                              int(window), int(n_sink), _p(out), _p(lse), _p(ws), _size(ws),
+                                              int(skip_tile), int(limit_ns), _stream(stream)))
+
+
+def vc_debug_draft_fp4_abort(sh, fc, q, out, lse, ws, stuck_warp: int, limit_ns: int, window: int = 0, n_sink: int = 0,
+                             stream=None):
+    """vc_draft_attn_fp4 with the first copies of warp stuck_warp of every
+    block never counted as landed, its waits giving up after limit_ns (see
+    include/vc.h)."""
+    _check(lib().vc_debug_draft_fp4_abort(ctypes.byref(sh), ctypes.byref(fc), int(window), int(n_sink), _p(q), _p(out),
+                                          _p(lse), _p(ws), _size(ws), int(stuck_warp), int(limit_ns), _stream(stream)))
 
 
 def vc_debug_quant_partition(sh, qc, target_blocks: int) -> dict:

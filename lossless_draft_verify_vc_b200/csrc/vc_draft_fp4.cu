@@ -138,7 +138,7 @@ struct FTile {
         a.q + (static_cast<int64_t>(b) * a.s.Hq + h * a.s.g + head) * D + i4 * (D / 4));
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) {
-      const uint4 v = head < a.s.g ? src[x] : make_uint4(0, 0, 0, 0);
+      const uint4 v = head < a.s.g ? stream::load_16(src + x) : make_uint4(0, 0, 0, 0);
       qf[4 * x] = v.x, qf[4 * x + 1] = v.y, qf[4 * x + 2] = v.z, qf[4 * x + 3] = v.w;
     }
     kup = two_to(a.k_exp, h, 1);

@@ -88,12 +88,28 @@ __host__ __device__ inline Span make_span(uint32_t L, uint32_t nq, uint32_t wind
   return p;
 }
 
+// Loads of what the call before may have written (see above), through L1 but
+// never the read-only path, whatever the compiler can prove.
+__device__ __forceinline__ uint32_t load_word(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 load_16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Request b's length as stored (a negative one is above every T_cap).
+__device__ __forceinline__ uint32_t stored_length(const Args& a, int b) { return load_word(a.lens + b); }
+
 template <int NR>
 __device__ __forceinline__ Span request_span(const Args& a, int b) {
   uint32_t L = a.T;
   if (a.lens) {
-    L = static_cast<uint32_t>(a.lens[b]);
-    if (L > a.T_cap) L = 0;  // (a negative length too)
+    L = stored_length(a, b);
+    if (L > a.T_cap) L = 0;
   }
   return make_span(L, a.nq, a.window, a.n_sink, NR);
 }
@@ -280,7 +296,7 @@ __device__ __forceinline__ void run(const Args& a, Tile& tile, unsigned char* st
   if (a.cluster) {  // rank r of a unit's C blocks: stages from ceil(r n / C)
     const int unit = k / a.cluster, rank = k - unit * a.cluster;
     b = unit / a.Hkv, h = unit - b * a.Hkv;
-    if (a.lens && tid == 0 && static_cast<uint32_t>(a.lens[b]) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
+    if (a.lens && tid == 0 && stored_length(a, b) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
     p = request_span<NR>(a, b);
     const uint32_t n = p.n, C = a.cluster;  // (the product stays below 2^31: at most 8 blocks)
     const int s0 = (rank * n + C - 1) / C;
@@ -294,7 +310,7 @@ __device__ __forceinline__ void run(const Args& a, Tile& tile, unsigned char* st
     if (a.lens) {
       int mine = 0;
       for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-        if (blockIdx.x == 0 && static_cast<uint32_t>(a.lens[b]) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
+        if (blockIdx.x == 0 && stored_length(a, b) > a.T_cap) atomicOr(a.flags, VC_FLAG_BAD_LENGTH);
         mine += (request_span<NR>(a, b).n + PAD) * a.Hkv;
       }
       int x = mine;

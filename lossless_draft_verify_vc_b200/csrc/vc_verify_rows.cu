@@ -104,7 +104,7 @@ struct RTile {
         a.q + ((static_cast<int64_t>(b) * a.s.nq + i) * a.s.Hq + h * a.s.g + head) * D + i4 * (D / 4));
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) {
-      qs[32 * x] = i < a.s.nq ? src[x] : make_uint4(0, 0, 0, 0);  // read by this lane alone
+      qs[32 * x] = i < a.s.nq ? stream::load_16(src + x) : make_uint4(0, 0, 0, 0);  // read by this lane alone
     }
   }
 

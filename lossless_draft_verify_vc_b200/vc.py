@@ -54,6 +54,7 @@ class vc_sparse_cache(Structure):
 class vc_fp4_cache(Structure):
     _fields_ = [("records", c_void_p), ("T_cap", c_int64), ("T", c_int64), ("lens", c_void_p), ("k_exp", c_void_p),
                 ("v_exp", c_void_p)]
+    _dims, _dev = None, -1  # (B, Hkv, D) and device, where fp4_cache made the descriptor
 
 
 class vc_sched_request(Structure):
@@ -366,9 +367,11 @@ def _fp4_dims(sh, fc, dev):
     """(B, Hkv, D) after checking a descriptor from fp4_cache against the shape
     and the current device (dev; -1: a tensor that is refused anyway)."""
     dims = sh.B, sh.Hkv, sh.D
-    if getattr(fc, "_dims", dims) != dims:
+    if fc._dims == dims and fc._dev == dev:
+        return dims
+    if fc._dims is not None and fc._dims != dims:
         raise ValueError(f"the cache holds (B, Hkv, D) = {fc._dims}, the shape says {dims}")
-    if getattr(fc, "_dev", dev) != dev >= 0:
+    if fc._dev >= 0 and dev >= 0 and fc._dev != dev:
         raise ValueError(f"the cache is on CUDA device {fc._dev}, the current device is {dev}")
     return dims
 

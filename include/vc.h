@@ -367,8 +367,10 @@ VC_API vc_status vc_fp4_cache_read(const vc_attn_shape* shape, const vc_fp4_cach
  *   window >= 0, n_sink >= 0 (without effect when window == 0).
  *   ws   workspace of vc_draft_attn_fp4_workspace_size() bytes.  Calls of
  *        this operator and of vc_verify_attn_window, of any shapes, may use
- *        one workspace of the largest size one after the other; one that
- *        another entry point wrote to has to be zero-filled again. */
+ *        one workspace of the largest size one after the other, and so may
+ *        vc_fp4_cache_write and vc_fp4_cache_read (which touch its flag word
+ *        only); one that another entry point wrote to has to be zero-filled
+ *        again. */
 VC_API size_t vc_draft_attn_fp4_workspace_size(const vc_attn_shape* shape, const vc_fp4_cache* cache);
 VC_API vc_status vc_draft_attn_fp4(const vc_attn_shape* shape, const vc_fp4_cache* cache, int64_t window,
                                    int64_t n_sink, const void* q, float* out, float* lse, void* ws, size_t ws_bytes,

@@ -96,7 +96,8 @@ struct FTile {
   // as 32 stages; counted as nothing the blocks that hold parts of two units
   // finish last.  Measured on B200, us of device time per call at 8 requests x
   // 32K and 1 x 262K: 8 stages 62.5, 62.4; 24 59.7, 58.1; 32 59.2, 57.7; 40
-  // 58.9, 57.7 (but one unit of 65K 19.6 against 18.4).
+  // 58.9, 57.7 (but one unit of 65K 19.6 against 18.4).  D = 64 takes the same
+  // numbers: its stages have the same bytes and products.
   static constexpr int PAD = 32;
   static constexpr int MIN = 48;  // padding and a short unit (16 stages)
   static constexpr int GAIN = 40;  // see stream::choose

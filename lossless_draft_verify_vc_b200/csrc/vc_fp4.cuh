@@ -9,7 +9,6 @@ namespace vc {
 namespace fp4 {
 
 constexpr int kTok = 16;  // tokens per record
-constexpr int kBlk = 16;  // channels per scale
 
 template <int D>
 struct Rec {
@@ -17,7 +16,6 @@ struct Rec {
   static constexpr int V = 8 * D;    // value codes
   static constexpr int KS = 16 * D;  // key scales
   static constexpr int VS = 17 * D;  // value scales
-  static constexpr int BLKS = D / kBlk;
 };
 
 // 8 e2m1 codes of a word -> 4 x f16x2 (channel pairs, exact).  Pass whole

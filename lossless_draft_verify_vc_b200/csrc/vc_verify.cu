@@ -55,7 +55,8 @@
 // tile that no row sees (past the request's length, or past the first n_sink
 // keys) may hold anything: the softmax warps clear them in shared memory
 // before P.V, since 0 * NaN would reach every row.  Warps of a row tile without a
-// query row (one-row calls, the second row tile of g = 5) only keep step.
+// query row (blocks of 9 to 96 rows, the second row tile of g = 5 to 7) only
+// keep step.
 // Up to 8 chunks of a unit run as one thread-block cluster and merge in it:
 // every block leaves its O rows and (m, l) in shared memory, and after a
 // cluster barrier sums its share of the rows from all of them (no partials
@@ -65,7 +66,11 @@
 // that waits on its own round trips (load, S, softmax, P.V) rather than on one
 // unit: ALU pipe 34%, tensor pipe 33%, issue 39%.  Without any softmax work it
 // took 34.6 us (g = 5, window 16000: 52.3 of 54.2), without the low parts'
-// product 38.1 (53.1), without both 31.2 (43.9).  Key tiles of 128 with one S
+// product 38.1 (53.1), without both 31.2 (43.9).  C is planned for the longest
+// request the shape allows and a block holds one unit's tiles, so shares are
+// uneven: 256 of 296 block slots are used, each with 17 tiles where 14.3 would
+// do (g = 5, window 16000, lengths 20001 and 9020: 32 or 18 tiles where 21.6
+// would).  Key tiles of 128 with one S
 // buffer took 48 us, two warpgroups per row 48, two warpgroups taking turns at
 // the tiles 43.5 (61.9), the same with one block per SM, 4 S buffers and 5
 // stages 50 (85).

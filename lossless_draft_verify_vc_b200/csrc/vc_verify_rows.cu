@@ -17,7 +17,8 @@
 // tcgen05 form against this one: 1 row, g = 4, 8 KV heads, window 1024 10.4 :
 // 7.2, window 8192 16.0 : 13.6, 8 requests with window 4096 33.1 : 27.8; 16
 // requests with window 512 16.5 : 10.0; 2 rows, 2 KV heads, window 4096 10.5 :
-// 10.5; but one KV head of 200K keys 31.2 : 34.0 (148 partials of one unit).
+// 10.5; but one KV head of 200K keys 31.2 : 34.0 (148 partials of one unit,
+// merged by half a block), which keeps this form for its exact weights.
 #include <algorithm>
 
 #include "vc_stream.cuh"
@@ -71,7 +72,8 @@ struct RTile {
   static constexpr int Q_OFF = stream::kWarps * stream::State<D>::bytes(COLS);
   static constexpr int SMEM_B = Q_OFF + stream::kWarps * (D / 32) * 512;
   static_assert(2 * stream::kMergeB <= SMEM_B, "the final merges' buffers take this place");
-  // a unit's begin in stages (8 KB, D = 128) and the least share, as in the 4-bit draft
+  // a unit's begin in stages (8 KB, D = 128) and the least share, as in the
+  // 4-bit draft; measured at D = 128, used for D = 64 too
   static constexpr int PAD = 8;
   static constexpr int MIN = 24;
   static constexpr int GAIN = 64;

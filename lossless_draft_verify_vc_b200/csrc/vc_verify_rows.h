@@ -6,6 +6,9 @@
 
 namespace vc {
 
+// The rule has no length in it: at most 8 rows keep all 24 bits of a weight
+// (include/vc.h), whatever the context.  It is the faster form too, but for one
+// KV head over a very long context (times in vc_verify_rows.cu).
 inline bool verify_rows_apply(const vc_attn_shape& sh, int nq) { return nq * (sh.Hq / sh.Hkv) <= 8; }
 size_t verify_rows_workspace(const vc_attn_shape& sh, int nq);
 // Arguments checked by the caller.

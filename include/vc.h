@@ -365,6 +365,8 @@ VC_API vc_status vc_fp4_cache_read(const vc_attn_shape* shape, const vc_fp4_cach
  *   out  fp32 [B][Hq][D];  lse  fp32 [B][Hq] natural-log softmax
  *        denominators, or NULL.  L == 0: a zero row, lse -inf.
  *   window >= 0, n_sink >= 0 (without effect when window == 0).
+ *   A weight of the softmax is kept to 22 significant bits; the tensor cores'
+ *   sums over long contexts are off by about 1e-6 of sum p |v|.
  *   ws   workspace of vc_draft_attn_fp4_workspace_size() bytes.  Calls of
  *        this operator and of vc_verify_attn_window, of any shapes, may use
  *        one workspace of the largest size one after the other, and so may

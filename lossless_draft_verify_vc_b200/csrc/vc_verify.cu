@@ -64,7 +64,7 @@
 // rows, g = 4, window 4096; 141 MB): 38.9 us of device time against 21.6 at
 // the copy rate: 9 us of start, drain and merge, and a tile loop at 4.7 TB/s
 // that waits on its own round trips (load, S, softmax, P.V) rather than on one
-// unit: ALU pipe 34%, tensor pipe 33%, issue 39%.  Without any softmax work it
+// unit: ALU pipe 29%, tensor pipe 34%, issue 38%.  Without any softmax work it
 // took 34.6 us (g = 5, window 16000: 52.3 of 54.2), without the low parts'
 // product 38.1 (53.1), without both 31.2 (43.9).  C is planned for the longest
 // request the shape allows and a block holds one unit's tiles, so shares are
